@@ -48,10 +48,11 @@
  *   - Size limits (checked on the host, SMOE_ERR_INVALID_ARG beyond them):
  *       routed entry points (smoe_route, smoe_route_bwd, smoe_mlp_*):
  *         1 <= k <= min(E, SMOE_MAX_TOPK), E <= SMOE_MAX_ROUTED_EXPERTS;
- *       sort and ParallelLinear (smoe_sort, smoe_sort_static,
- *         parallel_linear_*): E <= SMOE_MAX_EXPERTS;
+ *       sort, ParallelLinear and routing from logits (smoe_sort, smoe_sort_static,
+ *         parallel_linear_*, smoe_route_select*): E <= SMOE_MAX_EXPERTS;
  *       everywhere: T * k (the slot count) <= INT32_MAX, and every [rows, cols]
- *         tensor the call touches has fewer than 2^31 elements.
+ *         tensor the call touches has fewer than 2^31 elements (the paged cache
+ *         may be larger: its offsets are 64-bit).
  */
 #ifndef SMOE_H_
 #define SMOE_H_
@@ -148,6 +149,52 @@ int smoe_route(const void* x, const void* w_r, const float* b_r, int T, int d, i
 int smoe_route_bwd(const void* x, const void* w_r, const int32_t* topk_idx, const float* gates,
                    const float* dgates, int T, int d, int E, int k, smoe_dtype dt, void* dx,
                    float* dw_r, float* db_r, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing from given logits (the pages give no score function beyond top-k
+ * routing; this is the family of routers in use next to smoe_route's)
+ *
+ * smoe_route_select: per token, scores s_e of E experts from their logits,
+ *   SMOE_SCORE_SOFTMAX: s_e = exp(l_e) / sum_u exp(l_u)
+ *   SMOE_SCORE_SIGMOID: s_e = 1 / (1 + exp(-l_e)),
+ * ranked by c_e = s_e + bias[e] (bias NULL: by the logits).  With groups > 1 the
+ * experts lie in `groups` runs of E / groups; a group's rank is the sum of its
+ * group_top (1 or 2) best c, and only experts of the best top_groups groups are
+ * candidates.  The k best candidates are selected in descending order and
+ *   gates[t,j] = scale * s_e, or with renorm scale * s_e / (sum of the selected s).
+ * Whole numbers: groups and experts are those of an evaluation in 64 bits; equal
+ * values go to the lower id.
+ *   A logit of -inf or NaN, or a bias of -inf or NaN, makes its expert
+ *   unavailable: it ranks behind every other (lower id first), and when too few
+ *   others are left to fill k it is selected with gate 0, so that the ids of a row
+ *   are always distinct and in range (an empty row: all gates 0).  A logit of +inf
+ *   counts as the largest finite value.
+ *   logits [T, E] dtype with row stride ld (elements, >= E)   bias [E] fp32 or NULL
+ *   topk_idx [T, k] int32 (out)      gates [T, k] fp32 (out)
+ * Requires E <= SMOE_MAX_EXPERTS, E % groups == 0, groups <= SMOE_MAX_GROUPS,
+ * 1 <= k <= min(SMOE_MAX_TOPK, top_groups * E / groups), scale > 0 and finite.
+ * The outputs feed smoe_sort as smoe_route's do.
+ *
+ * smoe_route_select_bwd: the gradient of the logits (ids fixed; the bias takes
+ * none) from the forward's topk_idx and gates and from dgates [T, k] fp32.  With
+ * A = sum_i gates_i dgates_i:
+ *   softmax:        dl_e = [e selected] g_e dg_e - s_e A          (every expert)
+ *   softmax renorm: dl_e = g_e dg_e - g_e A / scale               (selected, else 0)
+ *   sigmoid:        dl_e = g_e dg_e (1 - s_e)                     (selected, else 0)
+ *   sigmoid renorm: dl_e = (g_e dg_e - g_e A / scale) (1 - s_e)   (selected, else 0)
+ *   dlogits [T, E] dtype (contiguous, overwritten).  A gate of 0 passes nothing on.
+ *   An id outside [0, E) is skipped and reported (SMOE_ERR_DATA); the ids of a row
+ *   must be distinct, as the forward's are.
+ * ------------------------------------------------------------------------ */
+typedef enum { SMOE_SCORE_SOFTMAX = 0, SMOE_SCORE_SIGMOID = 1 } smoe_score;
+#define SMOE_MAX_GROUPS 64
+
+int smoe_route_select(const void* logits, int ld, const float* bias, int T, int E, int k, int score,
+                      int renorm, float scale, int groups, int top_groups, int group_top,
+                      smoe_dtype dt, int32_t* topk_idx, float* gates, void* stream);
+int smoe_route_select_bwd(const void* logits, int ld, const int32_t* topk_idx, const float* gates,
+                          const float* dgates, int T, int E, int k, int score, int renorm,
+                          float scale, smoe_dtype dt, void* dlogits, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Reordering [src: "reordering operations"; rev1: grouped = expert-sorted]
@@ -274,6 +321,116 @@ int smoe_moa_attn_bwd(const void* q, const void* k, const void* v, const void* o
                       const void* dout, const int32_t* sorted_slot, int T, int L, int kslots, int heads,
                       int head_dim, smoe_dtype dt, void* dq, void* dk, void* dv, void* workspace,
                       size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Mixture-of-Attention: norm and rotation of queries and keys (this library's
+ * choice: the pages give the attention layer no position encoding)
+ *
+ * smoe_moa_qk_norm_rope_fwd: for every head x of head_dim values of q and of k
+ *   u = w x / sqrt(mean(x^2) + eps)                       (norm = 1; else u = x)
+ *   (y_a, y_b) = (u_a cos t - u_b sin t, u_b cos t + u_a sin t)   (inv_freq != NULL)
+ * with t = positions[token] * inv_freq[i] for pair i < head_dim / 2, (a, b) =
+ * (i, i + head_dim/2), or (2i, 2i+1) when interleaved.  A frequency of 0 leaves its
+ * pair as it is (partial rotation).  Angles keep their precision at far positions
+ * (whole turns are dropped in 64-bit fixed point).  One rounding, to dtype.
+ *   q [T*kslots, q_heads*head_dim] dtype: row i is slot p = sorted_slot[i] (grouped
+ *   rows; NULL: row i is slot i) of token p / kslots;  k [T, kv_heads*head_dim] in
+ *   token order; q_out, k_out like q, k, contiguous, and may be q, k themselves when
+ *   those are contiguous.  ldq, ldk: row strides in elements (multiples of 16
+ *   bytes).  positions [T] int32; inv_freq [head_dim/2] fp32 (finite); wq, wk
+ *   [head_dim] fp32, shared by the heads (NULL: 1).  q and q_out, or k and k_out,
+ *   may both be NULL.
+ * Requires head_dim 64 or 128, eps > 0 with norm.  A slot outside [0, T*kslots) is
+ * skipped and reported.
+ *
+ * smoe_moa_qk_norm_rope_bwd: from dyq, dyk (like q_out, k_out; row strides lddyq,
+ * lddyk) and the forward's q, k: dq, dk (contiguous, overwritten), and dwq, dwk
+ * [head_dim] fp32 (overwritten; NULL to skip), summed in an order fixed by the sizes.
+ * A part (q with dyq, dq, dwq; k likewise) is left out when its dy is NULL.
+ * workspace: smoe_moa_qk_norm_rope_bwd_workspace_size(desc) bytes.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int T, kslots, q_heads, kv_heads, head_dim;
+  int dtype;       /* smoe_dtype */
+  int norm;        /* 1: RMS norm per head */
+  int interleaved; /* pairs (2i, 2i+1) instead of (i, i + head_dim/2) */
+  float eps;
+} smoe_qk_desc;
+
+int smoe_moa_qk_norm_rope_fwd(const smoe_qk_desc* desc, const void* q, int64_t ldq, const void* k,
+                              int64_t ldk, const int32_t* sorted_slot, const int32_t* positions,
+                              const float* inv_freq, const float* wq, const float* wk, void* q_out,
+                              void* k_out, void* stream);
+size_t smoe_moa_qk_norm_rope_bwd_workspace_size(const smoe_qk_desc* desc);
+int smoe_moa_qk_norm_rope_bwd(const smoe_qk_desc* desc, const void* dyq, int64_t lddyq,
+                              const void* dyk, int64_t lddyk, const void* q, int64_t ldq,
+                              const void* k, int64_t ldk, const int32_t* sorted_slot,
+                              const int32_t* positions, const float* inv_freq, const float* wq,
+                              const float* wk, void* dq, void* dk, float* dwq, float* dwk,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Mixture-of-Attention over a paged cache: the serving form of the core
+ *
+ * smoe_kv_cache: keys and values of B sequences in pages of page_size tokens.
+ * Token u of sequence b lies in page block_table[b * table_stride + u / page_size]
+ * at offset u % page_size; head h of it at
+ *   k + page * k_page_stride + offset * k_token_stride + h * k_head_stride
+ * (elements; head_dim of them in a row; any order of page, token and head).  bf16,
+ * or with k_scale and v_scale (both, [num_pages, page_size, kv_heads] fp32) e4m3
+ * codes of one byte, a value being code * scale: scale = amax / 448 of the head's
+ * row (1 for an all-zero row), as smoe_quantize_weights_fp8's.
+ * seq_lens[b]: tokens of sequence b, the new ones included; 0 marks an unused row of
+ * the batch.  Entries of block_table beyond a sequence's pages are not read.
+ *
+ * smoe_moa_cache_append: norm and rotation (as above, at the token's place in its
+ * sequence; norm = 0 and inv_freq NULL for neither) of q, written to q_out, and of
+ * k, stored in the cache with v.  Row t of k and v is the newest token of sequence t
+ * (starts NULL, T == B), or for prompts a token of the sequence b with starts[b] <=
+ * t < starts[b+1] (starts [B+1] int32, ascending), which hold the last starts[b+1] -
+ * starts[b] tokens of sequence b.  Rows outside every sequence and of unused batch
+ * rows are left as they were, in q_out and in the cache.  A sequence shorter than its
+ * new tokens, a length beyond max_pages * page_size, or a page outside
+ * [0, num_pages) is skipped and reported (SMOE_ERR_DATA).  q and q_out may be NULL.
+ * Two new tokens must not share a cache place (two sequences that name one page);
+ * if they do, that place holds a mixture.  bf16 rows; desc.T counts the rows of k.
+ *
+ * smoe_moa_decode: attention of the newest token of each sequence (its kslots
+ * queries, grouped rows as in smoe_moa_attn_fwd) over its seq_lens cached tokens:
+ *   o[i, h] = sum_u softmax_u(<q[i, h], k[u, h']> / sqrt(head_dim)) v[u, h']
+ * with h' = h / (q_heads / kv_heads) (q_heads a multiple of kv_heads), and lse
+ * [B*kslots, q_heads] fp32 (NULL to skip) as smoe_moa_attn_fwd's.  An unused batch
+ * row gets o = 0 and lse = -inf.  A length outside [0, max_pages * page_size] is
+ * clamped, a key on a page outside [0, num_pages) is left out, a slot that
+ * sorted_slot does not name is not written; all three are reported.
+ *   q, o [B*kslots, q_heads*head_dim] bf16 (q's row stride ldq; o contiguous).
+ * workspace: smoe_moa_decode_workspace_size(B, kslots, q_heads, kv_heads, head_dim)
+ * bytes, 256-byte aligned; nothing in it is kept between calls.  The sums run in an
+ * order fixed by the sizes and lengths: equal calls give equal bits.
+ * Both require head_dim 64 or 128, max_pages * page_size <= 2^30, strides that are
+ * multiples of 16 bytes (else SMOE_ERR_INVALID_ARG), dtype bf16 (SMOE_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale; /* NULL: bf16 cache */
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens; /* [B] */
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int64_t table_stride;
+  int num_pages, page_size, max_pages, B, kv_heads, head_dim;
+} smoe_kv_cache;
+
+int smoe_moa_cache_append(const smoe_qk_desc* desc, const void* q, int64_t ldq, const void* k,
+                          int64_t ldk, const void* v, int64_t ldv, const int32_t* sorted_slot,
+                          const int32_t* starts, const float* inv_freq, const float* wq,
+                          const float* wk, const smoe_kv_cache* cache, void* q_out, void* stream);
+size_t smoe_moa_decode_workspace_size(int B, int kslots, int q_heads, int kv_heads, int head_dim);
+int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int kslots, int q_heads,
+                    const smoe_kv_cache* cache, void* o, float* lse, void* workspace,
+                    size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * SMoE MLP [abs, art: SMoE layer = top-k routing + weighted sum of expert MLPs]

@@ -766,6 +766,303 @@ int smoe_moa_attn_bwd(const void* q, const void* k, const void* v, const void* o
   return SMOE_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Routing from given logits
+// ---------------------------------------------------------------------------
+static int validate_select(int ld, int T, int E, int k, int score, float scale, int dt) {
+  if (T < 0 || E <= 0 || k <= 0) return fail(SMOE_ERR_INVALID_ARG, "bad sizes T=%d E=%d k=%d", T, E, k);
+  if (E > SMOE_MAX_EXPERTS || k > E || k > SMOE_MAX_TOPK)
+    return fail(SMOE_ERR_INVALID_ARG, "need 1 <= k <= min(E, %d), E <= %d (k=%d E=%d)", SMOE_MAX_TOPK,
+                SMOE_MAX_EXPERTS, k, E);
+  if (ld < E) return fail(SMOE_ERR_INVALID_ARG, "the row stride of logits is below E");
+  if (!slots_fit(T, k) || (long long)T * ld >= (1LL << 31))
+    return fail(SMOE_ERR_INVALID_ARG, "T*k or the logits too large for 32-bit indexing");
+  if (score != SMOE_SCORE_SOFTMAX && score != SMOE_SCORE_SIGMOID)
+    return fail(SMOE_ERR_INVALID_ARG, "score must be SOFTMAX or SIGMOID");
+  if (!(scale > 0.0f && scale <= 3.4e38f)) return fail(SMOE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (!valid_dtype(dt)) return fail(SMOE_ERR_INVALID_ARG, "bad dtype %d", dt);
+  return SMOE_OK;
+}
+
+int smoe_route_select(const void* logits, int ld, const float* bias, int T, int E, int k, int score,
+                      int renorm, float scale, int groups, int top_groups, int group_top,
+                      smoe_dtype dt, int32_t* topk_idx, float* gates, void* stream) {
+  smoe::NvtxScope nvtx_scope("smoe_route_select");
+  int rc = validate_select(ld, T, E, k, score, scale, dt);
+  if (rc != SMOE_OK) return rc;
+  if (groups < 1 || groups > SMOE_MAX_GROUPS || E % groups || top_groups < 1 || top_groups > groups)
+    return fail(SMOE_ERR_INVALID_ARG, "need 1 <= top_groups <= groups <= %d and E %% groups == 0",
+                SMOE_MAX_GROUPS);
+  if (group_top != 1 && group_top != 2) return fail(SMOE_ERR_INVALID_ARG, "group_top must be 1 or 2");
+  if (k > top_groups * (E / groups))
+    return fail(SMOE_ERR_INVALID_ARG, "k = %d is above the %d experts of top_groups groups", k,
+                top_groups * (E / groups));
+  if (T == 0) return SMOE_OK;
+  NEED(logits, "logits"); NEED(topk_idx, "topk_idx"); NEED(gates, "gates");
+  ALIGNED(logits, "logits");
+  SelectArgs a;
+  a.bias = bias; a.T = T; a.E = E; a.k = k; a.ld = ld; a.score = score; a.renorm = renorm != 0;
+  a.scale = scale; a.groups = groups; a.top_groups = top_groups; a.group_top = group_top;
+  cudaStream_t s = (cudaStream_t)stream;
+  PROF("route_select", 1);
+  SMOE_TRY(launch_select(logits, a, dt, topk_idx, gates, s), "smoe_route_select launch");
+  return SMOE_OK;
+}
+
+int smoe_route_select_bwd(const void* logits, int ld, const int32_t* topk_idx, const float* gates,
+                          const float* dgates, int T, int E, int k, int score, int renorm,
+                          float scale, smoe_dtype dt, void* dlogits, void* stream) {
+  smoe::NvtxScope nvtx_scope("smoe_route_select_bwd");
+  int rc = validate_select(ld, T, E, k, score, scale, dt);
+  if (rc != SMOE_OK) return rc;
+  if (T == 0) return SMOE_OK;
+  NEED(logits, "logits"); NEED(topk_idx, "topk_idx"); NEED(gates, "gates");
+  NEED(dgates, "dgates"); NEED(dlogits, "dlogits");
+  ALIGNED(logits, "logits"); ALIGNED(dlogits, "dlogits");
+  cudaError_t st;
+  unsigned* err = error_word(&st);
+  if (!err) return cuda_fail(st, "smoe_route_select_bwd");
+  SelectArgs a;
+  a.T = T; a.E = E; a.k = k; a.ld = ld; a.score = score; a.renorm = renorm != 0; a.scale = scale;
+  cudaStream_t s = (cudaStream_t)stream;
+  PROF("route_select_bwd", 1);
+  SMOE_TRY(launch_select_bwd(logits, a, dt, topk_idx, gates, dgates, dlogits, err, s),
+           "smoe_route_select_bwd launch");
+  return SMOE_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Query/key norm and rotation, paged cache, decode
+// ---------------------------------------------------------------------------
+static int validate_qk(const smoe_qk_desc* m) {
+  if (!m) return fail(SMOE_ERR_INVALID_ARG, "desc is NULL");
+  if (m->T < 0 || m->kslots < 1 || m->q_heads < 1 || m->kv_heads < 1)
+    return fail(SMOE_ERR_INVALID_ARG, "bad sizes T=%d kslots=%d q_heads=%d kv_heads=%d", m->T,
+                m->kslots, m->q_heads, m->kv_heads);
+  if (!valid_dtype(m->dtype)) return fail(SMOE_ERR_INVALID_ARG, "bad dtype %d", m->dtype);
+  if (m->head_dim != 64 && m->head_dim != 128)
+    return fail(SMOE_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", m->head_dim);
+  if (!slots_fit(m->T, m->kslots) ||
+      (long long)m->T * m->kslots >= (1LL << 31) / m->q_heads / m->head_dim ||
+      (long long)m->T >= (1LL << 31) / m->kv_heads / m->head_dim)
+    return fail(SMOE_ERR_INVALID_ARG, "tensor too large for 32-bit row indexing");
+  if (m->norm && !(m->eps > 0.0f)) return fail(SMOE_ERR_INVALID_ARG, "norm needs eps > 0");
+  return SMOE_OK;
+}
+static int validate_rows(const void* p, int64_t ld, int64_t width, int es, const char* name) {
+  if (!p) return SMOE_OK;
+  if (!aligned16(p)) return fail(SMOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (ld < width || ld * es % 16)
+    return fail(SMOE_ERR_INVALID_ARG, "the row stride of %s must be at least its width and a multiple of 16 bytes", name);
+  return SMOE_OK;
+}
+#define ROWS(p, ld, width, es, name)                                              \
+  do {                                                                            \
+    int rc_ = validate_rows(p, ld, width, es, name);                              \
+    if (rc_ != SMOE_OK) return rc_;                                               \
+  } while (0)
+
+static QkArgs qk_args(const smoe_qk_desc& m, const int32_t* sorted_slot, const float* inv_freq,
+                      const float* wq, const float* wk) {
+  QkArgs a;
+  a.T = m.T; a.kslots = m.kslots; a.q_heads = m.q_heads; a.kv_heads = m.kv_heads;
+  a.norm = m.norm != 0; a.interleaved = m.interleaved != 0; a.eps = m.eps;
+  a.sorted_slot = sorted_slot; a.inv_freq = inv_freq; a.wq = wq; a.wk = wk;
+  return a;
+}
+
+int smoe_moa_qk_norm_rope_fwd(const smoe_qk_desc* desc, const void* q, int64_t ldq, const void* k,
+                              int64_t ldk, const int32_t* sorted_slot, const int32_t* positions,
+                              const float* inv_freq, const float* wq, const float* wk, void* q_out,
+                              void* k_out, void* stream) {
+  smoe::NvtxScope nvtx_scope("smoe_moa_qk_norm_rope_fwd");
+  int rc = validate_qk(desc);
+  if (rc != SMOE_OK) return rc;
+  const smoe_qk_desc& m = *desc;
+  if (!m.norm && !inv_freq) return fail(SMOE_ERR_INVALID_ARG, "neither norm nor rotation asked for");
+  if (!m.norm && (wq || wk)) return fail(SMOE_ERR_INVALID_ARG, "weights need norm = 1");
+  if (m.T == 0) return SMOE_OK;
+  if (!q && !k) return fail(SMOE_ERR_INVALID_ARG, "q and k are NULL");
+  if (!q != !q_out || !k != !k_out) return fail(SMOE_ERR_INVALID_ARG, "a part needs its input and its output");
+  if (inv_freq) NEED(positions, "positions");
+  const int es = (int)esize((smoe_dtype)m.dtype);
+  ROWS(q, ldq, (int64_t)m.q_heads * m.head_dim, es, "q");
+  ROWS(k, ldk, (int64_t)m.kv_heads * m.head_dim, es, "k");
+  if (q) ALIGNED(q_out, "q_out");
+  if (k) ALIGNED(k_out, "k_out");
+  if ((q && q == q_out && ldq != (int64_t)m.q_heads * m.head_dim) ||
+      (k && k == k_out && ldk != (int64_t)m.kv_heads * m.head_dim))
+    return fail(SMOE_ERR_INVALID_ARG, "in place needs contiguous rows");
+  cudaError_t st;
+  unsigned* err = error_word(&st);
+  if (!err) return cuda_fail(st, "smoe_moa_qk_norm_rope_fwd");
+  QkArgs a = qk_args(m, sorted_slot, inv_freq, wq, wk);
+  a.q = q; a.ldq = ldq; a.k = k; a.ldk = ldk; a.positions = positions;
+  a.q_out = q_out; a.k_out = k_out; a.err = err;
+  cudaStream_t s = (cudaStream_t)stream;
+  PROF("moa.qk_norm_rope", 1);
+  SMOE_TRY(launch_qk_fwd(a, m.head_dim, (smoe_dtype)m.dtype, s), "smoe_moa_qk_norm_rope_fwd launch");
+  return SMOE_OK;
+}
+
+size_t smoe_moa_qk_norm_rope_bwd_workspace_size(const smoe_qk_desc* desc) {
+  if (validate_qk(desc) != SMOE_OK) return 0;
+  return qk_bwd_partial_floats(desc->T, desc->kslots, desc->q_heads, desc->kv_heads, desc->head_dim) *
+         sizeof(float);
+}
+
+int smoe_moa_qk_norm_rope_bwd(const smoe_qk_desc* desc, const void* dyq, int64_t lddyq,
+                              const void* dyk, int64_t lddyk, const void* q, int64_t ldq,
+                              const void* k, int64_t ldk, const int32_t* sorted_slot,
+                              const int32_t* positions, const float* inv_freq, const float* wq,
+                              const float* wk, void* dq, void* dk, float* dwq, float* dwk,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  smoe::NvtxScope nvtx_scope("smoe_moa_qk_norm_rope_bwd");
+  int rc = validate_qk(desc);
+  if (rc != SMOE_OK) return rc;
+  const smoe_qk_desc& m = *desc;
+  if (!m.norm && !inv_freq) return fail(SMOE_ERR_INVALID_ARG, "neither norm nor rotation asked for");
+  if (!m.norm && (wq || wk || dwq || dwk)) return fail(SMOE_ERR_INVALID_ARG, "weights need norm = 1");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (m.T == 0) {
+    if (dwq) SMOE_TRY(cudaMemsetAsync(dwq, 0, m.head_dim * sizeof(float), s), "qk_bwd zero dwq");
+    if (dwk) SMOE_TRY(cudaMemsetAsync(dwk, 0, m.head_dim * sizeof(float), s), "qk_bwd zero dwk");
+    return SMOE_OK;
+  }
+  if (!dyq && !dyk) return fail(SMOE_ERR_INVALID_ARG, "dyq and dyk are NULL");
+  if ((!dyq && (dq || dwq)) || (!dyk && (dk || dwk)))
+    return fail(SMOE_ERR_INVALID_ARG, "a gradient asked for needs its upstream gradient");
+  if (m.norm && ((dyq && !q) || (dyk && !k))) return fail(SMOE_ERR_INVALID_ARG, "the norm's backward needs q and k");
+  if (inv_freq) NEED(positions, "positions");
+  const int es = (int)esize((smoe_dtype)m.dtype);
+  const int64_t wide_q = (int64_t)m.q_heads * m.head_dim, wide_k = (int64_t)m.kv_heads * m.head_dim;
+  ROWS(dyq, lddyq, wide_q, es, "dyq"); ROWS(dyk, lddyk, wide_k, es, "dyk");
+  if (m.norm && dyq) ROWS(q, ldq, wide_q, es, "q");
+  if (m.norm && dyk) ROWS(k, ldk, wide_k, es, "k");
+  if (dq) ALIGNED(dq, "dq");
+  if (dk) ALIGNED(dk, "dk");
+  const size_t need = smoe_moa_qk_norm_rope_bwd_workspace_size(desc);
+  if ((dwq || dwk) && (!workspace || ws_bytes < need))
+    return fail(SMOE_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws_bytes, need);
+  if (dwq || dwk) ALIGNED(workspace, "workspace");
+  cudaError_t st;
+  unsigned* err = error_word(&st);
+  if (!err) return cuda_fail(st, "smoe_moa_qk_norm_rope_bwd");
+  QkArgs a = qk_args(m, sorted_slot, inv_freq, wq, wk);
+  a.dyq = dyq; a.lddyq = lddyq; a.dyk = dyk; a.lddyk = lddyk;
+  a.q = dyq ? (q ? q : dyq) : nullptr; a.ldq = ldq;  // a part is there when its dy is
+  a.k = dyk ? (k ? k : dyk) : nullptr; a.ldk = ldk;
+  a.positions = positions; a.q_out = dq; a.k_out = dk; a.dwq = dwq; a.dwk = dwk;
+  a.partial = (float*)workspace; a.err = err;
+  PROF("moa.qk_norm_rope_bwd", dwq || dwk ? 2 : 1);
+  SMOE_TRY(launch_qk_bwd(a, m.head_dim, (smoe_dtype)m.dtype, s), "smoe_moa_qk_norm_rope_bwd launch");
+  return SMOE_OK;
+}
+
+static int validate_cache(const smoe_kv_cache* c) {
+  if (!c) return fail(SMOE_ERR_INVALID_ARG, "cache is NULL");
+  if (c->B < 0 || c->num_pages < 0 || c->page_size < 1 || c->max_pages < 0 || c->kv_heads < 1)
+    return fail(SMOE_ERR_INVALID_ARG, "bad cache sizes");
+  if ((long long)c->max_pages * c->page_size > (1LL << 30))
+    return fail(SMOE_ERR_INVALID_ARG, "max_pages * page_size is above 2^30");
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(SMOE_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", c->head_dim);
+  if (!c->k_scale != !c->v_scale) return fail(SMOE_ERR_INVALID_ARG, "k_scale and v_scale go together");
+  if (c->table_stride < c->max_pages) return fail(SMOE_ERR_INVALID_ARG, "table_stride is below max_pages");
+  const int es = c->k_scale ? 1 : 2;
+  const int64_t st[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
+                         c->v_page_stride, c->v_token_stride, c->v_head_stride};
+  for (int64_t v : st)
+    if (v < 0 || v * es % 16) return fail(SMOE_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+  if (c->B == 0) return SMOE_OK;
+  NEED(c->seq_lens, "seq_lens");
+  if (c->max_pages > 0) NEED(c->block_table, "block_table");
+  if (c->num_pages > 0) { NEED(c->k, "k cache"); NEED(c->v, "v cache"); }
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(SMOE_ERR_INVALID_ARG, "the cache is not 16-byte aligned");
+  return SMOE_OK;
+}
+
+int smoe_moa_cache_append(const smoe_qk_desc* desc, const void* q, int64_t ldq, const void* k,
+                          int64_t ldk, const void* v, int64_t ldv, const int32_t* sorted_slot,
+                          const int32_t* starts, const float* inv_freq, const float* wq,
+                          const float* wk, const smoe_kv_cache* cache, void* q_out, void* stream) {
+  smoe::NvtxScope nvtx_scope("smoe_moa_cache_append");
+  int rc = validate_qk(desc);
+  if (rc != SMOE_OK) return rc;
+  if ((rc = validate_cache(cache)) != SMOE_OK) return rc;
+  const smoe_qk_desc& m = *desc;
+  if (m.dtype != SMOE_BF16) return fail(SMOE_ERR_UNSUPPORTED, "the cache takes bf16 rows");
+  if (m.kv_heads != cache->kv_heads || m.head_dim != cache->head_dim)
+    return fail(SMOE_ERR_INVALID_ARG, "desc and cache differ in kv_heads or head_dim");
+  if (!starts && m.T != cache->B) return fail(SMOE_ERR_INVALID_ARG, "without starts T must be the cache's B");
+  if (!m.norm && (wq || wk)) return fail(SMOE_ERR_INVALID_ARG, "weights need norm = 1");
+  if (m.T == 0 || cache->B == 0) return SMOE_OK;
+  NEED(k, "k"); NEED(v, "v");
+  if (!q != !q_out) return fail(SMOE_ERR_INVALID_ARG, "q and q_out go together");
+  const int64_t wide_q = (int64_t)m.q_heads * m.head_dim, wide_k = (int64_t)m.kv_heads * m.head_dim;
+  ROWS(q, ldq, wide_q, 2, "q"); ROWS(k, ldk, wide_k, 2, "k"); ROWS(v, ldv, wide_k, 2, "v");
+  if (q) ALIGNED(q_out, "q_out");
+  if (q && q == q_out && ldq != wide_q) return fail(SMOE_ERR_INVALID_ARG, "in place needs contiguous rows");
+  cudaError_t st;
+  unsigned* err = error_word(&st);
+  if (!err) return cuda_fail(st, "smoe_moa_cache_append");
+  QkArgs a = qk_args(m, sorted_slot, inv_freq, wq, wk);
+  a.q = q; a.ldq = ldq; a.k = k; a.ldk = ldk; a.v = v; a.ldv = ldv;
+  a.q_out = q_out; a.cache = cache; a.starts = starts; a.err = err;
+  cudaStream_t s = (cudaStream_t)stream;
+  PROF("moa.cache_append", 1);
+  SMOE_TRY(launch_cache_append(a, s), "smoe_moa_cache_append launch");
+  return SMOE_OK;
+}
+
+static size_t moa_decode_ws(int B, int kslots, int G, int head_dim) {
+  return align256(decode_workspace_bytes(G, head_dim)) + align256((size_t)B * kslots * sizeof(int32_t));
+}
+
+size_t smoe_moa_decode_workspace_size(int B, int kslots, int q_heads, int kv_heads, int head_dim) {
+  if (B < 0 || kslots < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads ||
+      (head_dim != 64 && head_dim != 128) || !slots_fit(B, kslots) ||
+      (long long)kslots * (q_heads / kv_heads) > 0x7fffffffLL)
+    return 0;
+  return moa_decode_ws(B, kslots, kslots * (q_heads / kv_heads), head_dim);
+}
+
+int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int kslots, int q_heads,
+                    const smoe_kv_cache* cache, void* o, float* lse, void* workspace,
+                    size_t ws_bytes, void* stream) {
+  smoe::NvtxScope nvtx_scope("smoe_moa_decode");
+  int rc = validate_cache(cache);
+  if (rc != SMOE_OK) return rc;
+  const smoe_kv_cache& c = *cache;
+  if (kslots < 1 || kslots > 128 || q_heads < 1 || q_heads % c.kv_heads)
+    return fail(SMOE_ERR_INVALID_ARG, "need 1 <= kslots <= 128 and q_heads a multiple of kv_heads");
+  if (!slots_fit(c.B, kslots) || (long long)c.B * kslots >= (1LL << 31) / q_heads / c.head_dim)
+    return fail(SMOE_ERR_INVALID_ARG, "tensor too large for 32-bit row indexing");
+  if (c.B == 0) return SMOE_OK;
+  NEED(q, "q"); NEED(o, "o");
+  ROWS(q, ldq, (int64_t)q_heads * c.head_dim, 2, "q");
+  ALIGNED(o, "o");
+  const int G = kslots * (q_heads / c.kv_heads);
+  const size_t need = moa_decode_ws(c.B, kslots, G, c.head_dim);
+  if (!workspace || ws_bytes < need)
+    return fail(SMOE_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws_bytes, need);
+  if (((uintptr_t)workspace & 255u) != 0) return fail(SMOE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  cudaError_t st;
+  unsigned* err = error_word(&st);
+  if (!err) return cuda_fail(st, "smoe_moa_decode");
+  cudaStream_t s = (cudaStream_t)stream;
+  int32_t* inv = nullptr;
+  if (sorted_slot) {
+    inv = (int32_t*)((char*)workspace + align256(decode_workspace_bytes(G, c.head_dim)));
+    PROF("moa.invert", 1);
+    SMOE_TRY(cudaMemsetAsync(inv, 0xff, (size_t)c.B * kslots * sizeof(int32_t), s), "moa decode invert");
+    SMOE_TRY(launch_invert(sorted_slot, c.B * kslots, inv, s), "moa decode invert");
+  }
+  PROF("moa.decode", 2);
+  SMOE_TRY(launch_decode(q, ldq, c, inv, kslots, q_heads, o, lse, workspace, err, s), "smoe_moa_decode");
+  return SMOE_OK;
+}
+
 int smoe_quantize_weights_fp8(const void* w, int E, int K, int N, smoe_dtype dt, uint8_t* codes,
                               float* scales, void* stream) {
   smoe::NvtxScope nvtx_scope("smoe_quantize_weights_fp8");

@@ -156,6 +156,50 @@ cudaError_t launch_attn_dkv(const void* q, const void* k, const void* v, const f
                             const void* dout, const int32_t* inv, int T, int L, int kslots, int heads,
                             void* dk, void* dv, const float* dsum, unsigned* err, cudaStream_t s);
 
+// Routing from given logits (select.cu).
+struct SelectArgs {
+  const float* bias = nullptr;  // [E] added to the scores that are ranked, nullable
+  int T = 0, E = 0, k = 0, ld = 0;
+  int score = SMOE_SCORE_SOFTMAX, renorm = 1;
+  float scale = 1.0f;
+  int groups = 1, top_groups = 1, group_top = 2;
+};
+cudaError_t launch_select(const void* logits, const SelectArgs& a, smoe_dtype dt, int32_t* idx,
+                          float* gates, cudaStream_t s);
+cudaError_t launch_select_bwd(const void* logits, const SelectArgs& a, smoe_dtype dt,
+                              const int32_t* idx, const float* gates, const float* dgates, void* dl,
+                              unsigned* err, cudaStream_t s);
+
+// Query/key norm and rotation, and the paged cache (qk_norm.cu).
+struct QkArgs {
+  int T = 0, kslots = 1, q_heads = 0, kv_heads = 0;
+  int norm = 0, interleaved = 0;
+  float eps = 0.0f;
+  const void *q = nullptr, *k = nullptr, *v = nullptr;       // rows; null parts are left out
+  const void *dyq = nullptr, *dyk = nullptr;                 // backward: upstream gradients
+  int64_t ldq = 0, ldk = 0, ldv = 0, lddyq = 0, lddyk = 0;   // row strides, elements
+  const int32_t* sorted_slot = nullptr;  // slot of each q row (null: row i is slot i)
+  const int32_t* positions = nullptr;    // [T] (training form)
+  const float* inv_freq = nullptr;       // [head_dim / 2] (null: no rotation)
+  const float *wq = nullptr, *wk = nullptr;  // [head_dim] (null: 1)
+  void *q_out = nullptr, *k_out = nullptr;   // contiguous rows
+  float *dwq = nullptr, *dwk = nullptr, *partial = nullptr;
+  // serving form: k and v go to the cache
+  const smoe_kv_cache* cache = nullptr;  // host copy
+  const int32_t* starts = nullptr;       // [B+1] first row of each sequence (null: row b)
+  unsigned* err = nullptr;
+};
+size_t qk_bwd_partial_floats(int T, int kslots, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_qk_fwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s);
+cudaError_t launch_qk_bwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s);
+cudaError_t launch_cache_append(const QkArgs& a, cudaStream_t s);
+
+// Paged decode attention (decode.cu).  inv: grouped row of each slot (null: row = slot).
+size_t decode_workspace_bytes(int G, int head_dim);
+cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, const int32_t* inv,
+                          int kslots, int q_heads, void* o, float* lse, void* ws, unsigned* err,
+                          cudaStream_t s);
+
 // e4m3 quantisation (fp8.cu): rows of a bf16 [rows, cols] matrix with one scale per
 // row; weights [E, K, N] bf16 -> codes [E, N, K] with one scale per (e, column)
 cudaError_t launch_quantize_rows_fp8(const void* x, int rows, int cols, uint8_t* codes, float* scales,

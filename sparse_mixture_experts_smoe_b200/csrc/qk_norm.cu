@@ -1,0 +1,482 @@
+// qk_norm.cu -- RMS norm of queries and keys for each head with the position rotation
+// in the same pass, forward and backward (smoe_moa_qk_norm_rope_fwd / _bwd), and its
+// serving form, which stores keys and values in a paged cache (smoe_moa_cache_append).
+//
+//   u = w x / sqrt(mean(x^2) + eps)      per head of head_dim values, fp32
+//   (y_a, y_b) = (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = position * inv_freq
+//   backward, with du = the upstream gradient turned back by t and r = 1/sqrt(...):
+//   dw = sum du x r,   dx = r (w du - x r mean(w du x r))
+//
+// One pass over the data: a lane holds two 16-byte pieces of a head, V values from its
+// first half and V from its second (V = 8 bf16, 4 fp32), so that a pair is always in one
+// lane: (i, head_dim/2 + i), or (2i, 2i + 1) when interleaved.  head_dim / (2V) lanes
+// share a head; the mean is log2 of that many shuffles.  A lane keeps its row's cosines
+// and sines for all heads of the row.
+//
+// Angles: far positions need more than fp32.  inv_freq / (2 pi) is held as a 64-bit
+// fixed-point fraction of a turn, so position * fraction modulo 2^64 is the angle with
+// whole turns dropped exactly; its upper 32 bits go to sincospif.
+#include "tc_ptx.cuh"
+
+namespace smoe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 4 * 148;  // of the backward, per part: fixes the order of dw's sums
+
+template <typename T>
+struct Geo {
+  static constexpr int V = 16 / sizeof(T);  // values per 16-byte piece
+};
+
+__device__ __forceinline__ void load_piece(const float* p, float* v) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+}
+__device__ __forceinline__ void load_piece(const bf16* p, float* v) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void store_piece(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_piece(bf16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = pack8(v);
+}
+
+template <int LPH>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int off = LPH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  return v;
+}
+template <int LPH>
+__device__ __forceinline__ float head_max(float v) {
+#pragma unroll
+  for (int off = LPH / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+  return v;
+}
+
+// Fraction of a turn per position, modulo one turn, in units of 2^-64.
+__device__ __forceinline__ unsigned long long turn_fraction(float inv_freq) {
+  double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+  t -= floor(t);
+  return (unsigned long long)(t * 18446744073709551616.0);
+}
+__device__ __forceinline__ void turn(unsigned long long f, int pos, float* c, float* s) {
+  const unsigned long long a = f * (unsigned long long)(long long)pos;
+  const int hi = (int)(unsigned)((a + 0x80000000ull) >> 32);  // turns * 2^32, in [-1/2, 1/2)
+  sincospif((float)hi * 4.656612873077393e-10f, s, c);        // hi 2^-31 = turns * 2
+}
+
+// Frequency index of pair i (i < V) of lane `sub`.
+template <typename T, int DH, bool kInter>
+__device__ __forceinline__ int pair_freq(int sub, int i) {
+  constexpr int V = Geo<T>::V;
+  if (!kInter) return sub * V + i;
+  return i < V / 2 ? sub * (V / 2) + i : DH / 4 + sub * (V / 2) + i - V / 2;
+}
+// Turns the lane's 2V values x (first V: piece a, last V: piece b) by its V pairs.
+template <int V, bool kInter>
+__device__ __forceinline__ void rotate(float* x, const float* c, const float* s, float sign) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int p = kInter ? 2 * i : i, q = kInter ? 2 * i + 1 : V + i;
+    const float a = x[p], b = x[q], sn = sign * s[i];
+    x[p] = a * c[i] - b * sn;
+    x[q] = b * c[i] + a * sn;
+  }
+}
+
+// Where the rows of a part come from and what happens to them.
+enum Part : int { PART_Q = 0, PART_K = 1, PART_V = 2 };
+
+struct KArgs {
+  QkArgs a;
+  smoe_kv_cache c;  // serving form
+  int nb[3];        // blocks of each part
+  int hpu;          // heads a unit (a group of lanes) walks through
+};
+
+// Position (and cache slot) of token t in the serving form.  False: leave the row as
+// it is (padding, or a data error, which is reported).
+__device__ __forceinline__ bool serving_place(const KArgs& g, int t, int* pos, int64_t* page, int* off) {
+  const smoe_kv_cache& c = g.c;
+  int b = t, after = 1;  // rows of the sequence from this one on
+  if (g.a.starts) {
+    if (t < g.a.starts[0] || t >= g.a.starts[c.B]) return false;  // rows outside every sequence
+    int lo = 0, hi = c.B - 1;  // the last sequence that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (g.a.starts[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    after = g.a.starts[b + 1] - t;
+  } else if (c.seq_lens[b] == 0) {
+    return false;  // an unused row of the batch
+  }
+  const int len = c.seq_lens[b];
+  const long long p = (long long)len - after;
+  if (after <= 0 || p < 0 || len > (long long)c.max_pages * c.page_size) {
+    report_error(g.a.err, ERRBIT_DATA);
+    return false;
+  }
+  *pos = (int)p;
+  const int in_table = (int)p / c.page_size;
+  const int id = c.block_table[(int64_t)b * c.table_stride + in_table];
+  if (id < 0 || id >= c.num_pages) {
+    report_error(g.a.err, ERRBIT_DATA);
+    return false;
+  }
+  *page = id;
+  *off = (int)p - in_table * c.page_size;
+  return true;
+}
+
+__device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <typename T, int DH, bool kInter, bool kServe>
+__global__ void __launch_bounds__(kThreads)
+qk_fwd_kernel(const __grid_constant__ KArgs g) {
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH;
+  const QkArgs& a = g.a;
+  int part = PART_Q, blk = blockIdx.x;
+  while (part < PART_V && blk >= g.nb[part]) blk -= g.nb[part++];
+  const int heads = part == PART_Q ? a.q_heads : a.kv_heads;
+  const int rows = part == PART_Q ? a.T * a.kslots : a.T;
+  const T* x = (const T*)(part == PART_Q ? a.q : part == PART_K ? a.k : a.v);
+  const int64_t ldx = part == PART_Q ? a.ldq : part == PART_K ? a.ldk : a.ldv;
+  const float* wp = part == PART_Q ? a.wq : a.wk;
+  const bool norm = a.norm && part != PART_V, rot = a.inv_freq && part != PART_V;
+  const int sub = threadIdx.x % LPH, chunks = cdiv(heads, g.hpu);
+  const long long units = (long long)rows * chunks;
+
+  float w[2 * V];
+  unsigned long long fr[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    w[i] = w[V + i] = 1.0f;
+    if (norm && wp) {
+      w[i] = wp[sub * V + i];
+      w[V + i] = wp[DH / 2 + sub * V + i];
+    }
+    fr[i] = rot ? turn_fraction(a.inv_freq[pair_freq<T, DH, kInter>(sub, i)]) : 0ull;
+  }
+
+  // the loop count is the same for all lanes of a block: the head sums shuffle whole warps
+  const long long first = (long long)blk * UPB, step = (long long)g.nb[part] * UPB;
+  for (long long u0 = first; u0 < units; u0 += step) {
+    const long long u = u0 + threadIdx.x / LPH;
+    bool live = u < units;
+    const int row = live ? (int)(u / chunks) : 0;
+    const int h0 = live ? (int)(u % chunks) * g.hpu : 0;
+    int t = row, pos = 0, off = 0;
+    int64_t page = 0;
+    if (live && part == PART_Q) {
+      int p = row;
+      if (a.sorted_slot) p = a.sorted_slot[row];
+      if (p < 0 || p >= rows) {
+        report_error(a.err, ERRBIT_DATA);
+        live = false;
+      }
+      t = p / a.kslots;
+    }
+    if (kServe) live = live && serving_place(g, t, &pos, &page, &off);
+    else if (live && rot) pos = a.positions[t];
+    float c[V], s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      c[i] = 1.0f; s[i] = 0.0f;
+      if (rot) turn(fr[i], pos, &c[i], &s[i]);
+    }
+    const T* xr = x + row * ldx;
+#pragma unroll 4
+    for (int hh = 0; hh < g.hpu; ++hh) {
+      const int h = h0 + hh;
+      const bool on = live && h < heads;
+      float v[2 * V];
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) v[i] = 0.0f;
+      if (on) {
+        load_piece(xr + h * DH + sub * V, v);
+        load_piece(xr + h * DH + DH / 2 + sub * V, v + V);
+      }
+      if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) ss += v[i] * v[i];
+        const float r = 1.0f / sqrtf(head_sum<LPH>(ss) * (1.0f / DH) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) v[i] *= r * w[i];
+      }
+      if (rot) rotate<V, kInter>(v, c, s, 1.0f);
+      if (!kServe || part == PART_Q) {
+        if (on) {
+          T* out = (T*)(part == PART_Q ? a.q_out : a.k_out) + ((int64_t)row * heads + h) * DH;
+          store_piece(out + sub * V, v);
+          store_piece(out + DH / 2 + sub * V, v + V);
+        }
+      } else {
+        const bool is_k = part == PART_K;
+        const int64_t at = page * (is_k ? g.c.k_page_stride : g.c.v_page_stride) +
+                           off * (is_k ? g.c.k_token_stride : g.c.v_token_stride) +
+                           h * (is_k ? g.c.k_head_stride : g.c.v_head_stride);
+        if (g.c.k_scale == nullptr) {
+          if (on) {
+            T* out = (T*)(is_k ? g.c.k : g.c.v) + at;
+            store_piece(out + sub * V, v);
+            store_piece(out + DH / 2 + sub * V, v + V);
+          }
+        } else {  // one scale per (token, head): its largest magnitude maps to 448
+          float m = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) m = fmaxf(m, fabsf(v[i]));
+          m = head_max<LPH>(m);
+          const float sc = m > 0.0f ? m / 448.0f : 1.0f;
+          if (on) {
+            uint8_t* out = (uint8_t*)(is_k ? g.c.k : g.c.v) + at;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint16_t q[V / 2];
+#pragma unroll
+              for (int i = 0; i < V / 2; ++i)
+                q[i] = e4m3_pair(v[half * V + 2 * i] / sc, v[half * V + 2 * i + 1] / sc);
+              uint2 u8;
+              u8.x = q[0] | ((uint32_t)q[1] << 16);
+              u8.y = q[V / 2 - 2] | ((uint32_t)q[V / 2 - 1] << 16);
+              *reinterpret_cast<uint2*>(out + half * (DH / 2) + sub * V) = u8;
+            }
+            if (sub == 0)
+              (is_k ? g.c.k_scale : g.c.v_scale)[(page * g.c.page_size + off) * heads + h] = sc;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int DH, bool kInter>
+__global__ void __launch_bounds__(kThreads)
+qk_bwd_kernel(const __grid_constant__ KArgs g) {
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH;
+  __shared__ float red[kThreads / 32][DH];
+  const QkArgs& a = g.a;
+  const int part = (int)blockIdx.x < g.nb[0] ? PART_Q : PART_K;
+  const int blk = part == PART_Q ? blockIdx.x : blockIdx.x - g.nb[0];
+  const int heads = part == PART_Q ? a.q_heads : a.kv_heads;
+  const int rows = part == PART_Q ? a.T * a.kslots : a.T;
+  const T* x = (const T*)(part == PART_Q ? a.q : a.k);
+  const T* dy = (const T*)(part == PART_Q ? a.dyq : a.dyk);
+  const int64_t ldx = part == PART_Q ? a.ldq : a.ldk, ldy = part == PART_Q ? a.lddyq : a.lddyk;
+  T* dx = (T*)(part == PART_Q ? a.q_out : a.k_out);
+  const float* wp = part == PART_Q ? a.wq : a.wk;
+  const bool want_dw = (part == PART_Q ? a.dwq : a.dwk) != nullptr;
+  const bool rot = a.inv_freq != nullptr;
+  const int sub = threadIdx.x % LPH, chunks = cdiv(heads, g.hpu);
+  const long long units = (long long)rows * chunks;
+
+  float w[2 * V], dw[2 * V];
+  unsigned long long fr[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    w[i] = w[V + i] = 1.0f;
+    dw[i] = dw[V + i] = 0.0f;
+    if (wp) {
+      w[i] = wp[sub * V + i];
+      w[V + i] = wp[DH / 2 + sub * V + i];
+    }
+    fr[i] = rot ? turn_fraction(a.inv_freq[pair_freq<T, DH, kInter>(sub, i)]) : 0ull;
+  }
+  const long long first = (long long)blk * UPB, step = (long long)g.nb[part] * UPB;
+  for (long long u0 = first; u0 < units; u0 += step) {
+    const long long u = u0 + threadIdx.x / LPH;
+    bool live = u < units;
+    const int row = live ? (int)(u / chunks) : 0;
+    const int h0 = live ? (int)(u % chunks) * g.hpu : 0;
+    int t = row;
+    if (live && part == PART_Q) {
+      int p = row;
+      if (a.sorted_slot) p = a.sorted_slot[row];
+      if (p < 0 || p >= rows) {
+        report_error(a.err, ERRBIT_DATA);
+        live = false;
+      }
+      t = p / a.kslots;
+    }
+    const int pos = live && rot ? a.positions[t] : 0;
+    float c[V], s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      c[i] = 1.0f; s[i] = 0.0f;
+      if (rot) turn(fr[i], pos, &c[i], &s[i]);
+    }
+    const T* xr = x + row * ldx;
+    const T* yr = dy + row * ldy;
+#pragma unroll 2
+    for (int hh = 0; hh < g.hpu; ++hh) {
+      const int h = h0 + hh;
+      const bool on = live && h < heads;
+      float v[2 * V], d[2 * V];
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) v[i] = d[i] = 0.0f;
+      if (on) {
+        load_piece(yr + h * DH + sub * V, d);
+        load_piece(yr + h * DH + DH / 2 + sub * V, d + V);
+        if (a.norm) {
+          load_piece(xr + h * DH + sub * V, v);
+          load_piece(xr + h * DH + DH / 2 + sub * V, v + V);
+        }
+      }
+      if (rot) rotate<V, kInter>(d, c, s, -1.0f);
+      if (a.norm) {
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+          ss += v[i] * v[i];
+          dot += d[i] * w[i] * v[i];
+        }
+        ss = head_sum<LPH>(ss);
+        dot = head_sum<LPH>(dot);
+        const float r = 1.0f / sqrtf(ss * (1.0f / DH) + a.eps);
+        const float m = r * dot * (1.0f / DH);  // mean of (w du x r)
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+          const float hat = v[i] * r;
+          dw[i] += d[i] * hat;
+          d[i] = r * (w[i] * d[i] - hat * m);
+        }
+      }
+      if (on && dx) {
+        T* out = dx + ((int64_t)row * heads + h) * DH;
+        store_piece(out + sub * V, d);
+        store_piece(out + DH / 2 + sub * V, d + V);
+      }
+    }
+  }
+  if (!want_dw) return;
+  // this block's share of dw: lanes of equal `sub`, then the warps in order
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < 2 * V; ++i) {
+    float v = dw[i];
+#pragma unroll
+    for (int off = LPH; off < 32; off <<= 1) v += __shfl_xor_sync(kFull, v, off);
+    if (lane < LPH) red[warp][(i < V ? 0 : DH / 2 - V) + sub * V + i] = v;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < DH; i += kThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kThreads / 32; ++j) v += red[j][i];
+    a.partial[(size_t)blockIdx.x * DH + i] = v;
+  }
+}
+
+// dw[i] = sum of the blocks' shares: 32 columns by 32 block slices, joined in order.
+__global__ void __launch_bounds__(1024)
+qk_dw_sum_kernel(const float* __restrict__ partial, int nq, int nk, int DH, float* dwq, float* dwk) {
+  __shared__ float red[32][33];
+  const int per = DH / 32, part = blockIdx.x / per;
+  const int col = (blockIdx.x % per) * 32 + threadIdx.x;
+  float* out = part == 0 ? dwq : dwk;
+  const int b0 = part == 0 ? 0 : nq, nb = part == 0 ? nq : nk;
+  if (!out) return;
+  float v = 0.0f;
+  for (int b = threadIdx.y; b < nb; b += 32) v += partial[(size_t)(b0 + b) * DH + col];
+  red[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0) {
+    v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v += red[j][threadIdx.x];
+    out[col] = v;
+  }
+}
+
+// Blocks of a part of `rows` rows in units of hpu heads.
+int part_blocks(long long rows, int heads, int hpu, int upb, int most) {
+  const long long units = rows * cdiv(heads, hpu);
+  const long long n = (units + upb - 1) / upb;
+  return (int)(n < most ? n : most);
+}
+// Heads a unit walks through: all of the row's heads share its cosines and sines, but a
+// small batch spreads its heads over more lanes (148 SMs x 8 warps filled first).
+int heads_per_unit(long long rows, int heads, int lph) {
+  return rows * lph >= 148 * 256 ? heads : 1;
+}
+int lanes_per_head(int head_dim, int es) { return head_dim * es / 32; }
+
+void plan(KArgs& g, int head_dim, int es, int most) {
+  const QkArgs& a = g.a;
+  const int lph = lanes_per_head(head_dim, es), upb = kThreads / lph;
+  const int heads = a.q_heads > a.kv_heads ? a.q_heads : a.kv_heads;
+  g.hpu = heads_per_unit((long long)a.T * a.kslots, heads, lph);
+  g.nb[0] = a.q ? part_blocks((long long)a.T * a.kslots, a.q_heads, g.hpu, upb, most) : 0;
+  g.nb[1] = a.k ? part_blocks(a.T, a.kv_heads, g.hpu, upb, most) : 0;
+  g.nb[2] = a.v ? part_blocks(a.T, a.kv_heads, g.hpu, upb, most) : 0;
+}
+
+template <typename T, int DH>
+cudaError_t fwd(const KArgs& g, cudaStream_t s) {
+  const int grid = g.nb[0] + g.nb[1] + g.nb[2];
+  if (g.a.interleaved) qk_fwd_kernel<T, DH, true, false><<<grid, kThreads, 0, s>>>(g);
+  else qk_fwd_kernel<T, DH, false, false><<<grid, kThreads, 0, s>>>(g);
+  return cudaGetLastError();
+}
+template <int DH>
+cudaError_t append(const KArgs& g, cudaStream_t s) {
+  const int grid = g.nb[0] + g.nb[1] + g.nb[2];
+  if (g.a.interleaved) qk_fwd_kernel<bf16, DH, true, true><<<grid, kThreads, 0, s>>>(g);
+  else qk_fwd_kernel<bf16, DH, false, true><<<grid, kThreads, 0, s>>>(g);
+  return cudaGetLastError();
+}
+template <typename T, int DH>
+cudaError_t bwd(const KArgs& g, cudaStream_t s) {
+  const int grid = g.nb[0] + g.nb[1];
+  if (g.a.interleaved) qk_bwd_kernel<T, DH, true><<<grid, kThreads, 0, s>>>(g);
+  else qk_bwd_kernel<T, DH, false><<<grid, kThreads, 0, s>>>(g);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (!g.a.dwq && !g.a.dwk)) return e;
+  qk_dw_sum_kernel<<<2 * (DH / 32), dim3(32, 32), 0, s>>>(g.a.partial, g.nb[0], g.nb[1], DH,
+                                                          g.a.dwq, g.a.dwk);
+  return cudaGetLastError();
+}
+
+constexpr int kFwdBlocks = 8 * 148;
+
+}  // namespace
+
+size_t qk_bwd_partial_floats(int T, int kslots, int q_heads, int kv_heads, int head_dim) {
+  (void)T; (void)kslots; (void)q_heads; (void)kv_heads;
+  return (size_t)2 * kMaxBlocks * head_dim;
+}
+
+cudaError_t launch_qk_fwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s) {
+  KArgs g{};
+  g.a = a;
+  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4, kFwdBlocks);
+  if (dt == SMOE_BF16) return head_dim == 64 ? fwd<bf16, 64>(g, s) : fwd<bf16, 128>(g, s);
+  return head_dim == 64 ? fwd<float, 64>(g, s) : fwd<float, 128>(g, s);
+}
+
+cudaError_t launch_cache_append(const QkArgs& a, cudaStream_t s) {
+  KArgs g{};
+  g.a = a;
+  g.c = *a.cache;
+  plan(g, g.c.head_dim, 2, kFwdBlocks);
+  return g.c.head_dim == 64 ? append<64>(g, s) : append<128>(g, s);
+}
+
+cudaError_t launch_qk_bwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s) {
+  KArgs g{};
+  g.a = a;
+  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4, kMaxBlocks);
+  if (dt == SMOE_BF16) return head_dim == 64 ? bwd<bf16, 64>(g, s) : bwd<bf16, 128>(g, s);
+  return head_dim == 64 ? bwd<float, 64>(g, s) : bwd<float, 128>(g, s);
+}
+
+}  // namespace smoe

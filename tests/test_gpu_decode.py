@@ -1,0 +1,262 @@
+"""Attention of one new token over a paged cache (smoe_moa_decode) against a plain form in
+64 bits: ragged and empty batches, pages that end anywhere, both cache types, shared key
+heads, layouts, far offsets, bad tables, graphs and streams."""
+import math
+
+import pytest
+import torch
+
+import sparse_mixture_experts_smoe_b200 as smoe
+
+from . import _plain_ops as plain
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+# Relative error of a weight.  The score is an fp32 sum of 128 products of size at most 40
+# (2^-24 times a tree and a chain of under 16 roundings, 2^-15 of an exponent), ex2 2 ulp;
+# then the weight is rounded to bf16 for a bf16 cache, to fp16 with its scale for e4m3.
+SCORE = 2.0 ** -14
+WEIGHT = {False: 2.0 ** -8 + SCORE, True: 2.0 ** -11 + SCORE}
+
+CASES = {
+    # lens, page, kslots, q_heads, kv_heads, dh, e4m3, layout
+    "one_token": ([1], 16, 1, 1, 1, 128, False, "token"),
+    "one_sequence": ([2048], 16, 4, 4, 4, 128, False, "token"),
+    "ragged_and_empty": ([0, 5, 64, 0, 65, 1, 300, 0], 16, 4, 2, 2, 128, False, "token"),
+    "all_empty": ([0, 0, 0], 16, 2, 2, 1, 128, False, "token"),
+    "odd_pages": ([100, 33, 207], 7, 3, 3, 1, 64, False, "head"),
+    "page_of_one": ([50, 3], 1, 1, 2, 2, 64, False, "both"),
+    "page_of_100": ([1000, 99, 100, 101], 100, 2, 6, 2, 128, False, "head"),
+    "sixteen_queries": ([513, 40], 48, 8, 4, 2, 128, False, "both"),
+    "thirty_two_queries": ([700, 129], 64, 8, 4, 1, 128, False, "token"),
+    "ninety_queries": ([300, 64, 17], 32, 15, 12, 2, 128, False, "token"),
+    "many_sequences": ([(37 * b) % 91 for b in range(300)], 16, 2, 1, 1, 64, False, "token"),
+    "e4m3": ([300, 0, 64, 63], 48, 2, 8, 2, 128, True, "token"),
+    "e4m3_one": ([1], 7, 1, 1, 1, 64, True, "head"),
+    "e4m3_sixteen": ([400, 31], 16, 4, 4, 1, 64, True, "both"),
+    "e4m3_forty": ([260, 5], 100, 5, 8, 1, 128, True, "token"),
+    "e4m3_long": ([4099], 256, 4, 1, 1, 128, True, "token"),
+}
+
+
+def _store(x, layout):
+    """x [pages, page, kvh, dh] on the GPU in one of the layouts that strides allow."""
+    pages, page, kvh, dh = x.shape
+    if layout == "head":
+        return x.permute(0, 2, 1, 3).contiguous().cuda().permute(0, 2, 1, 3)
+    if layout == "both":
+        wide = torch.zeros((pages, 2, page, kvh, dh), dtype=x.dtype)
+        wide[:, 1] = x
+        return wide.cuda()[:, 1]
+    return x.cuda()
+
+
+def _problem(lens, page, ks, qh, kvh, dh, f8, layout, seed=0, qstd=1.0):
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 2
+    perm = torch.randperm(pages, generator=g).int()
+    table = torch.full((B, max(max(need), 1) + 1), -7, dtype=torch.int32)  # never read beyond need
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    p = dict(lens=lens, ks=ks, qh=qh, table=table, scales=(None, None))
+    used = torch.zeros(pages, page, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        u = torch.arange(n)
+        used[table[b, u // page].long(), u % page] = True
+    vals, stored, scales = [], [], []
+    for _ in range(2):
+        x = torch.randn(pages, page, kvh, dh, generator=g)
+        if f8:
+            s = (0.1 + torch.rand(pages, page, kvh, generator=g)) * x.abs().amax(-1) / 448.0
+            code = (x / s[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+            vals.append(code.double() * s.double()[..., None])
+            raw = code.view(torch.uint8).clone()
+            raw[~used] = 0x7f  # NaN
+            s[~used] = math.nan
+            stored.append(_store(raw, layout))
+            scales.append(s.cuda())
+        else:
+            x = x.to(BF)
+            vals.append(x.double())
+            x = x.clone()
+            x[~used] = math.nan  # places without a token are not read
+            stored.append(_store(x, layout))
+    if f8:
+        p["scales"] = tuple(scales)
+    p["k"], p["v"], p["kc"], p["vc"] = *vals, *stored
+    p["q"] = (qstd * torch.randn(B * ks, qh * dh, generator=g)).to(BF)
+    p["slots"] = torch.randperm(B * ks, generator=g).int()
+    return p
+
+
+def _args(p):
+    return dict(q=p["q"].cuda(), k_cache=p["kc"], v_cache=p["vc"], block_table=p["table"].cuda(),
+                seq_lens=torch.tensor(p["lens"], dtype=torch.int32, device="cuda"),
+                sorted_slot=p["slots"].cuda(), kslots=p["ks"], q_heads=p["qh"],
+                k_scale=p["scales"][0], v_scale=p["scales"][1])
+
+
+def _run(p, **kw):
+    return smoe.smoe_moa_decode(**{**_args(p), **kw})
+
+
+def _close(p, o, lse, rows=slice(None), table=None, lens=None):
+    ref, rl, size = plain.decode(p["q"], p["k"], p["v"], p["table"] if table is None else table,
+                                 p["lens"] if lens is None else lens, p["slots"], p["ks"], p["qh"])
+    f8 = p["scales"][0] is not None
+    # fp16 weights times scales below 2^-14 of the largest lose 2^-25 of it each: with at most
+    # 8192 keys of codes up to 448, and scales within 11 to 1, under 2^-9 of the mean weight's
+    # share of a row whose largest value is at most 4 times its mean size
+    tol = plain.HALF[BF] * ref.abs() + (WEIGHT[f8] + (2.0 ** -9 if f8 else 0.0)) * size
+    assert o.dtype == BF and o.shape == p["q"].shape
+    got = o.cpu().double()
+    assert torch.isfinite(got[rows]).all()
+    assert ((got - ref).abs() <= tol + 1e-30)[rows].all()
+    lse = lse.cpu().double()
+    fin = torch.isfinite(rl)
+    assert torch.equal(torch.isfinite(lse)[rows], fin[rows]) and (lse[rows][~fin[rows]] < 0).all()
+    err = (torch.where(fin, lse, torch.zeros_like(lse)) - torch.where(fin, rl, torch.zeros_like(rl))).abs()
+    assert (err <= SCORE + plain.HALF[torch.float32] * torch.where(fin, rl, torch.zeros_like(rl)).abs())[rows].all()
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_decode(name):
+    p = _problem(*CASES[name])
+    o, lse = _run(p)
+    assert smoe.smoe_check() == 0
+    _close(p, o, lse)
+    o2, lse2 = _run(p)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_decode_peaked_scores(f8):
+    """Queries along a key: one key in the middle takes nearly all of the weight, the
+    running maximum jumps, and the scores before it lose theirs."""
+    p = _problem([700, 64], 16, 2, 2, 1, 128, f8, "token", seed=2, qstd=0.05)
+    for b, u in ((0, 413), (1, 0)):
+        key = p["k"][int(p["table"][b, u // 16]), u % 16, 0]
+        for i in range(4):
+            if int(p["slots"][i]) // 2 == b:
+                p["q"][i] = (3.0 * key.repeat(2) / key.norm() * 11).to(BF)
+    o, lse = _run(p)
+    assert smoe.smoe_check() == 0
+    _close(p, o, lse)
+
+
+def test_decode_without_slots_rows_apart_and_no_lse():
+    p = _problem([70, 20, 9], 16, 2, 2, 2, 128, False, "token", seed=3)
+    p["slots"] = torch.arange(6, dtype=torch.int32)
+    o, lse = _run(p, sorted_slot=None)
+    _close(p, o, lse)
+    wide = torch.zeros(6, 256 + 64, dtype=BF, device="cuda")
+    wide[:, 32:288] = p["q"].cuda()
+    tab = torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+    tab[:, 5:5 + p["table"].shape[1]] = p["table"].cuda()
+    o2, _ = _run(p, q=wide[:, 32:288], block_table=tab[:, 5:5 + p["table"].shape[1]])
+    assert torch.equal(o, o2) and smoe.smoe_check() == 0
+    mine, ml = torch.empty_like(o), torch.empty_like(lse)
+    o3, l3 = _run(p, o=mine, lse=ml)
+    assert o3 is mine and l3 is ml and torch.equal(o3, o) and torch.equal(l3, lse)
+
+
+def test_decode_reports_bad_tables_lengths_and_slots():
+    p = _problem([40, 33, 16, 50], 16, 2, 1, 1, 64, False, "token", seed=4)
+    table = p["table"].clone()
+    table[0, 1] = 10 ** 6
+    table[2, 0] = -1           # every key of sequence 2 is left out
+    o, lse = _run(p, block_table=table.cuda())
+    assert smoe.smoe_check() == -4 and smoe.smoe_check() == 0
+    _close(p, o, lse, table=table)
+    # lengths are clamped to what the table can hold, and to 0
+    cap = p["table"].shape[1] * 16
+    lens = [40, -3, 16, cap + 9]
+    table = p["table"].clone()
+    table[3] = torch.arange(table.shape[1]) % 4
+    q = dict(p, table=table)
+    kc = torch.nan_to_num(p["kc"].float(), nan=0.5).to(BF)
+    vc = torch.nan_to_num(p["vc"].float(), nan=0.5).to(BF)
+    q.update(kc=kc, vc=vc, k=kc.cpu().double(), v=vc.cpu().double())
+    o, lse = _run(q, seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    assert smoe.smoe_check() == -4
+    _close(q, o, lse, lens=lens)
+    # a slot that no row names is not written; the others are right
+    slots = p["slots"].clone()
+    slots[1], slots[5] = -1, 99
+    o = torch.full_like(p["q"], 9.0).cuda()
+    lse = torch.full((8, 1), 9.0, device="cuda")
+    _run(p, sorted_slot=slots.cuda(), o=o, lse=lse)
+    assert smoe.smoe_check() == -4
+    keep = [i for i in range(8) if i not in (1, 5)]
+    _close(p, o, lse, rows=keep)
+    assert (o[[1, 5]] == 9).all() and (lse[[1, 5]] == 9).all()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_decode_offsets_beyond_32_bits(f8):
+    """Pages at the far end of a cache of more than 2^32 bytes (and 2^32 elements in
+    e4m3): the same bits as from a small cache that holds the same pages."""
+    p = _problem([150, 61], 64, 2, 2, 2, 128, f8, "token", seed=5)
+    o, lse = _run(p)
+    pages = p["kc"].shape[0]
+    far = 270000 if f8 else 140000  # x 64 x 2 x 128 elements
+    big = [torch.empty((far, 64, 2, 128), dtype=p["kc"].dtype, device="cuda") for _ in range(2)]
+    kw = {}
+    if f8:
+        sc = [torch.empty((far, 64, 2), device="cuda") for _ in range(2)]
+        for s, t in zip(sc, p["scales"]):
+            s[far - pages:] = t
+        kw = dict(k_scale=sc[0], v_scale=sc[1])
+    for b, t in zip(big, (p["kc"], p["vc"])):
+        b[far - pages:] = t
+    table = torch.where(p["table"] >= 0, p["table"] + (far - pages), p["table"])
+    o2, lse2 = _run(p, k_cache=big[0], v_cache=big[1], block_table=table.cuda(), **kw)
+    assert smoe.smoe_check() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_empty_batch():
+    c = torch.empty(0, 16, 1, 64, dtype=BF, device="cuda")
+    o, lse = smoe.smoe_moa_decode(torch.empty(0, 64, dtype=BF, device="cuda"), c, c,
+                                  torch.empty(0, 0, dtype=torch.int32, device="cuda"),
+                                  torch.empty(0, dtype=torch.int32, device="cuda"), None, 1, 1)
+    assert o.shape == (0, 64) and lse.shape == (0, 1)
+    # a cache without pages, a batch without tokens
+    o, lse = smoe.smoe_moa_decode(torch.ones(2, 64, dtype=BF, device="cuda"), c, c,
+                                  torch.empty(2, 0, dtype=torch.int32, device="cuda"),
+                                  torch.zeros(2, dtype=torch.int32, device="cuda"), None, 1, 1)
+    assert smoe.smoe_check() == 0
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+def test_decode_streams_and_graphs():
+    """Two streams at once, and two graphs with their own workspaces replayed in turn
+    while lengths and tables change under them."""
+    ps = [_problem([900, 33, 0, 257], 16, 4, 2, 2, 128, f8, "token", seed=6) for f8 in (False, True)]
+    args = [_args(p) for p in ps]
+    want = [smoe.smoe_moa_decode(**a) for a in args]
+    sts = [torch.cuda.Stream() for _ in ps]
+    for st in sts:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [smoe.smoe_moa_decode(stream=st, **a) for _ in range(3) for a, st in zip(args, sts)]
+    for st in sts:
+        st.synchronize()
+    for i, (o, lse) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+    graphs, outs = [], []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(smoe.smoe_moa_decode(**a))
+        graphs.append(g)
+    for lens in ([900, 33, 0, 257], [1, 0, 0, 2], [640, 16, 0, 200]):
+        for g, a, out in zip(graphs, args, outs):
+            a["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+            g.replay()
+            now = smoe.smoe_moa_decode(**a)
+            assert torch.equal(out[0], now[0]) and torch.equal(out[1], now[1])
+    assert smoe.smoe_check() == 0
