@@ -973,7 +973,8 @@ static int validate_cache(const smoe_kv_cache* c) {
   const int64_t st[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
                          c->v_page_stride, c->v_token_stride, c->v_head_stride};
   for (int64_t v : st)
-    if (v < 0 || v * es % 16) return fail(SMOE_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+    if (v < 0 || v * es % 16 || v * es / 16 > 0xffffffffLL)
+      return fail(SMOE_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes, below 2^36 bytes");
   if (c->B == 0) return SMOE_OK;
   NEED(c->seq_lens, "seq_lens");
   if (c->max_pages > 0) NEED(c->block_table, "block_table");
@@ -1015,16 +1016,12 @@ int smoe_moa_cache_append(const smoe_qk_desc* desc, const void* q, int64_t ldq, 
   return SMOE_OK;
 }
 
-static size_t moa_decode_ws(int B, int kslots, int G, int head_dim) {
-  return align256(decode_workspace_bytes(G, head_dim)) + align256((size_t)B * kslots * sizeof(int32_t));
-}
-
 size_t smoe_moa_decode_workspace_size(int B, int kslots, int q_heads, int kv_heads, int head_dim) {
   if (B < 0 || kslots < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads ||
       (head_dim != 64 && head_dim != 128) || !slots_fit(B, kslots) ||
       (long long)kslots * (q_heads / kv_heads) > 0x7fffffffLL)
     return 0;
-  return moa_decode_ws(B, kslots, kslots * (q_heads / kv_heads), head_dim);
+  return decode_workspace_bytes(B * kslots, kv_heads, kslots * (q_heads / kv_heads), head_dim);
 }
 
 int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int kslots, int q_heads,
@@ -1043,7 +1040,7 @@ int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int 
   ROWS(q, ldq, (int64_t)q_heads * c.head_dim, 2, "q");
   ALIGNED(o, "o");
   const int G = kslots * (q_heads / c.kv_heads);
-  const size_t need = moa_decode_ws(c.B, kslots, G, c.head_dim);
+  const size_t need = decode_workspace_bytes(c.B * kslots, c.kv_heads, G, c.head_dim);
   if (!workspace || ws_bytes < need)
     return fail(SMOE_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws_bytes, need);
   if (((uintptr_t)workspace & 255u) != 0) return fail(SMOE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
@@ -1051,15 +1048,8 @@ int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int 
   unsigned* err = error_word(&st);
   if (!err) return cuda_fail(st, "smoe_moa_decode");
   cudaStream_t s = (cudaStream_t)stream;
-  int32_t* inv = nullptr;
-  if (sorted_slot) {
-    inv = (int32_t*)((char*)workspace + align256(decode_workspace_bytes(G, c.head_dim)));
-    PROF("moa.invert", 1);
-    SMOE_TRY(cudaMemsetAsync(inv, 0xff, (size_t)c.B * kslots * sizeof(int32_t), s), "moa decode invert");
-    SMOE_TRY(launch_invert(sorted_slot, c.B * kslots, inv, s), "moa decode invert");
-  }
-  PROF("moa.decode", 2);
-  SMOE_TRY(launch_decode(q, ldq, c, inv, kslots, q_heads, o, lse, workspace, err, s), "smoe_moa_decode");
+  PROF("moa.decode", 3);
+  SMOE_TRY(launch_decode(q, ldq, c, sorted_slot, kslots, q_heads, o, lse, workspace, err, s), "smoe_moa_decode");
   return SMOE_OK;
 }
 

@@ -8,16 +8,25 @@
 // The cache is read once, so bytes bound it: 4 G head_dim operations against
 // 4 head_dim bytes (bf16) per key and head leave the tensor pipe far from busy.
 //
-// Split: the work is cut into units of 64 keys of one (sequence, key head) item; the
-// items' units in a row are dealt out in equal runs to a fixed number of CTAs, so a
-// ragged batch and a single long sequence load the GPU alike.  An item that a CTA holds
-// whole is finished there; the shares of the others go to the workspace and a second
-// kernel joins them in CTA order.  No atomics: a batch gives the same bits every time.
+// Split: a sequence is cut into units of 16 H keys (H = 2 where a row is 128 bytes or
+// less, which spreads a unit's own instructions over more keys).  The sequences' units in
+// a row, with kItemCost units' worth of time for a sequence's own start and end, are cut
+// into ranges; a job is a range and an item (a key head and a tile of queries), and a
+// warp's.  Neighbouring warps have the items of one range, because the key heads' rows of
+// a token lie next to one another in a page (64 sequences of up to 16384 bf16 tokens, 4
+// heads: 184 us, with ranges of single heads 188; 128 of 8000 in e4m3: 106 and 112).  No warp waits for another.  Seven eighths go in equal ranges, a job to each warp
+// of the GPU; the rest in smaller ones that a warp fetches from a counter when it has
+// finished, because SMs do not get equal shares of the memory's rate (equal runs alone
+// ended up to 20% apart).  So a ragged batch and a single long sequence load the GPU
+// alike (those 64 sequences: 184 us, without fetched ranges 193, with a quarter 191).  A
+// sequence that lies in one range is finished there; the shares of the others go
+// to the workspace and a second kernel joins them in the order of the ranges.  Ranges and
+// the order of all sums follow from sizes and lengths alone: a batch gives the same bits
+// every time.
 //
-// A CTA's four warps each take 16 keys of a unit and are independent until the item
-// ends: a warp copies its keys' rows with cp.async into its own ring in shared memory,
-// a few units ahead and across items, and keeps a running maximum m, sum l and
-// accumulator O of its own (one pass over the data):
+// A warp copies its keys' rows with cp.async into its own ring in shared memory, units
+// ahead and across items, and keeps a running maximum m, sum l and accumulator O (one
+// pass over the data):
 //   S^T = K Q^T      mma m16n8k16, keys as rows, 8 queries as columns
 //   m' = max(m, S), P = exp(S - m'), l = l e^(m-m') + sum P, O^T = O^T e^(m-m') + V^T P^T
 // Keys as rows cost ceil(G/8) 8-column products instead of a 16-row tile padded with
@@ -34,28 +43,42 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kKeys = 16;                    // keys of a warp's share of a unit
-constexpr int kUnit = kKeys * kWarps;        // keys of a unit
+constexpr int kHalf = 16;                    // keys of a product's tile
+constexpr int kItemCost = 2;                 // an item's start and end, in units
+constexpr int kLeast = 4;                    // units of a range, rather than more warps
+constexpr int kSpread = kThreads;            // runs of sequences that the units are counted for
+constexpr int kFifo = 8;                     // ranges between a warp's loads and its products
 
 struct DecArgs {
   const bf16* q;
   int64_t ldq;
-  const int32_t* inv;  // grouped row of each slot, or null: row = slot
+  const int32_t* slots;  // sorted_slot, or null: row = slot
+  const int32_t* inv;    // grouped row of each slot that a row names
   smoe_kv_cache c;
   int kslots, q_heads, group, G, mts;  // mts: query tiles of 8 NT rows
+  unsigned long long page_mul;         // position / page_size = position * page_mul >> page_shift
+  int page_shift;
+  int one_page;                        // 16 divides page_size
+  unsigned k_page, k_token, k_head, v_page, v_token, v_head;  // strides in 16-byte pieces
   float scale_log2;                    // log2(e) / sqrt(head_dim)
   bf16* o;
   float* lse;  // nullable
-  // shares of split items: [grid][2] slots of R rows, R = 8 NT
-  float* part_o;   // [grid][2][R][DH]
-  float* part_ml;  // [grid][2][R][2]
-  int4* desc;      // [grid]: item started and not ended here (b, item), last CTA of it or -1
+  // two shares for each job, of min(G, R) rows (R = 8 NT): of a sequence that an earlier
+  // range started, and of one that goes on in the next
+  int workers;         // warps
+  float* part_o;       // [jobs][2][rows][DH]
+  float* part_ml;      // [jobs][2][rows][2]
+  int4* split;         // [jobs] what several ranges hold: b, item, first and last range
+  unsigned* counts;    // ranges fetched, split items
   unsigned* err;
 };
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -107,22 +130,42 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Grouped row of each slot, no range taken and no split item.  Entries of slots that no
+// row names keep what they hold: a reader checks that the row it finds names the slot.
+__global__ void __launch_bounds__(256)
+decode_prepare_kernel(const int32_t* __restrict__ slots, int rows, int32_t* __restrict__ inv,
+                      unsigned* __restrict__ counts, unsigned* err) {
+  pdl_trigger();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < 2) counts[i] = 0;
+  if (slots == nullptr || i >= rows) return;
+  const int p = slots[i];
+  if (p >= 0 && p < rows) inv[p] = i;
+  else report_error(err, ERRBIT_DATA);
+}
+
 template <int DH, bool F8>
 struct Tile {
   static constexpr int kRow = F8 ? DH : 2 * DH;    // bytes of a cached row of a head
-  static constexpr int kChunks = kRow / 16;
-  static constexpr int kRows = 2 * kKeys * kRow;   // a warp's K rows, then its V rows
-  static constexpr int kStage = kRows + (F8 ? 2 * kKeys * 4 : 0);  // and their scales
-  // Byte of 16-byte chunk c of row r: eight rows of one chunk lie in eight different
-  // 16-byte bank groups, so that ldmatrix reads without conflicts.
-  static __device__ __forceinline__ uint32_t at(int r, int c) {
-    return (uint32_t)(r * kRow + ((c ^ (kChunks >= 8 ? (r & 7) : ((r >> 1) & 3))) << 4));
-  }
+  static constexpr int H = kRow <= 128 ? 2 : 1;
+  static constexpr int kUnit = kHalf * H;          // keys of a unit
+  // Eight rows' chunks of one number lie in eight bank groups: rows 16 bytes further apart
+  // than they are long, or (128 bytes, where room is short) chunk c of row r at c ^ (r & 7).
+  static constexpr bool kSwizzle = kRow == 128;
+  static constexpr int kPitch = kSwizzle ? kRow : kRow + 16;
+  static constexpr int kRows = 2 * kUnit * kPitch;                 // K rows, then V rows
+  static constexpr int kStage = kRows + (F8 ? 2 * kUnit * 4 : 0);  // and their scales
 };
 
-// A place in the row of units: unit `tile` of item `it` of sequence b.
+// A place in the row of units: unit `tile` of sequence b, for item it; `left` costs before
+// the end of the range (none: the range has no further unit).
 struct Cursor {
-  int b, it, tile, tiles, len;
+  int b, it, tile, tiles, len, left, range;
 };
 
 __device__ __forceinline__ int seq_len(const smoe_kv_cache& c, int b) {
@@ -130,60 +173,73 @@ __device__ __forceinline__ int seq_len(const smoe_kv_cache& c, int b) {
   const int n = c.seq_lens[b];
   return n < 0 ? 0 : (int)(n < cap ? n : cap);
 }
-__device__ __forceinline__ void next_unit(Cursor& p, const smoe_kv_cache& c, int items) {
+template <int UNIT>
+__device__ __forceinline__ int tiles_in(int len) { return (len + UNIT - 1) / UNIT; }
+
+template <int UNIT>
+__device__ __forceinline__ void next_unit(Cursor& p, const smoe_kv_cache& c) {
+  --p.left;
   if (++p.tile < p.tiles) return;
+  p.left -= kItemCost;
   p.tile = 0;
-  if (++p.it < items) return;
-  p.it = 0;
   do {
-    if (++p.b >= c.B) { p.len = 0; p.tiles = 1 << 30; return; }
+    if (++p.b >= c.B) { p.left = 0; return; }
     p.len = seq_len(c, p.b);
-    p.tiles = (p.len + kUnit - 1) / kUnit;
+    p.tiles = tiles_in<UNIT>(p.len);
   } while (p.tiles == 0);
 }
-
-// Row of o, q and lse of query n of query tile mt, key head kvh, sequence b; -1 for a
-// column that stands for no query (or a slot that sorted_slot leaves out: reported).
-__device__ __forceinline__ int query_row(const DecArgs& a, int b, int qi, int kvh, int* head) {
-  if (qi >= a.G) return -1;
-  *head = kvh * a.group + qi % a.group;
-  const int slot = b * a.kslots + qi / a.group;
-  if (!a.inv) return slot;
-  const int r = a.inv[slot];
-  if (r < 0 || r >= a.c.B * a.kslots) {
-    report_error(a.err, ERRBIT_DATA);
-    return -1;
-  }
-  return r;
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-template <int DH, int NT, bool F8, int STAGES>
-__global__ void __launch_bounds__(kThreads)
+// Slot and query head of query qi of key head kvh of sequence b.
+__device__ __forceinline__ int query_slot(const DecArgs& a, int b, int qi, int kvh, int* head) {
+  *head = kvh * a.group + qi % a.group;
+  return b * a.kslots + qi / a.group;
+}
+// Place (row * q_heads + head) of that query in o and lse; -1 for a column that stands for
+// no query, and for a slot that no row names (reported).
+__device__ __forceinline__ int query_place(const DecArgs& a, int b, int qi, int kvh) {
+  if (qi >= a.G) return -1;
+  int head;
+  const int slot = query_slot(a, b, qi, kvh, &head);
+  int row = slot;
+  if (a.slots) {
+    row = a.inv[slot];
+    if (row < 0 || row >= a.c.B * a.kslots || a.slots[row] != slot) {
+      report_error(a.err, ERRBIT_DATA);
+      return -1;
+    }
+  }
+  return row * a.q_heads + head;
+}
+
+template <int DH, int NT, bool F8, int STAGES, int PER_SM>
+__global__ void __launch_bounds__(kThreads, PER_SM)
 decode_kernel(const __grid_constant__ DecArgs a) {
   using TL = Tile<DH, F8>;
-  constexpr int R = 8 * NT, KS = DH / 16;
-  constexpr int RED = DH + 4;  // row pitch of the joining buffer: conflict-free
+  constexpr int R = 8 * NT, KS = DH / 16, H = TL::H, UNIT = TL::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* red = reinterpret_cast<float*>(smem + (size_t)kWarps * STAGES * TL::kStage);  // [R][RED]
-  float* mls = red + R * RED;                                                          // [warps][R][2]
   __shared__ unsigned masks[kWarps][STAGES];
+  __shared__ long long before[kSpread];  // costs before each run of sequences
   __shared__ long long wsum[kWarps];
-  __shared__ int s_b;
-  __shared__ long long s_rem;
+  __shared__ Cursor fifo[kWarps][kFifo];
 
   const smoe_kv_cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int items = c.kv_heads * a.mts;
   const int cta = blockIdx.x;
 
-  // ---- this CTA's run of units: [u0, u1) of all ------------------------------
-  const int per = (c.B + kThreads - 1) / kThreads;
-  const int bb0 = threadIdx.x * per, bb1 = min(c.B, bb0 + per);
+  // ---- the row of units: costs of the runs of sequences --------------------------
+  const int per = (c.B + kSpread - 1) / kSpread;
   long long mine = 0;
-  for (int b = bb0; b < bb1; ++b) {
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    if (b >= c.B) break;
     const int n = c.seq_lens[b];
     if (cta == 0 && (n < 0 || n > (long long)c.max_pages * c.page_size)) report_error(a.err, ERRBIT_DATA);
-    mine += (seq_len(c, b) + kUnit - 1) / kUnit;
+    const int t = tiles_in<UNIT>(seq_len(c, b));
+    mine += t > 0 ? t + kItemCost : 0;
   }
   long long incl = mine;
 #pragma unroll
@@ -193,59 +249,75 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   }
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += wsum[w];
+    if (w < warp) incl += wsum[w];
     total += wsum[w];
   }
-  const long long U = total * items;
-  const int ctas = (int)min((long long)gridDim.x, U);  // those with a run: no run is empty
-  const long long u0 = cta < ctas ? U * cta / ctas : 0;
-  const long long n_units = cta < ctas ? U * (cta + 1) / ctas - u0 : 0;
-  if (n_units > 0 && u0 >= before * items && u0 < (before + mine) * items) {
-    long long rem = u0 - before * items;
-    for (int b = bb0; b < bb1; ++b) {
-      const long long tu = (long long)((seq_len(c, b) + kUnit - 1) / kUnit) * items;
-      if (rem < tu) { s_b = b; s_rem = rem; break; }
-      rem -= tu;
-    }
-  }
+  before[threadIdx.x] = incl - mine;
   __syncthreads();
-
-  // sequences without a cached token: o = 0, lse = -inf
-  for (int b = cta; b < c.B; b += gridDim.x) {
-    if (seq_len(c, b) > 0) continue;
-    for (int i = threadIdx.x; i < a.G * c.kv_heads * (DH / 8); i += kThreads) {
-      int head;
-      const int row = query_row(a, b, i / (DH / 8) % a.G, i / (DH / 8) / a.G, &head);
-      if (row < 0) continue;
-      *reinterpret_cast<uint4*>(a.o + ((int64_t)row * a.q_heads + head) * DH + 8 * (i % (DH / 8))) =
-          make_uint4(0, 0, 0, 0);
-      if (a.lse && i % (DH / 8) == 0) a.lse[(int64_t)row * a.q_heads + head] = -INFINITY;
+  // costs of a range that is dealt out (nr of them, W jobs), and of one that is fetched
+  const int W = a.workers, nr = max(1, W / items);
+  const long long share = quotient(total, nr);
+  const bool fetch = share >= 8 * kLeast;
+  const int dealt = fetch ? (int)(share - share / 8) : max(kLeast, (int)share + 1);
+  const long long rest = total - (long long)nr * dealt;  // not above 0 without fetched ranges
+  const int fetched = fetch ? (int)quotient(rest + nr - 1, nr) : 1;
+  const int ranges = nr + (rest > 0 ? (int)quotient(rest + fetched - 1, fetched) : 0);
+  auto start_of = [&](int r) -> long long {
+    return r <= nr ? (long long)r * dealt : (long long)nr * dealt + (long long)(r - nr) * fetched;
+  };
+  auto range_of = [&](long long x) -> int {
+    const long long y = x - (long long)nr * dealt;
+    return (int)(y < 0 ? quotient(x, dealt) : nr + quotient(y, fetched));
+  };
+  // The first unit of a job, for a whole warp.
+  auto open_job = [&](unsigned job) -> Cursor {
+    Cursor p{};
+    p.range = job / items;
+    p.it = job - p.range * items;
+    const long long x = start_of(p.range), end = min(total, start_of(p.range + 1));
+    if (x >= end) return p;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kSpread / 32; ++i) n += before[i * 32 + lane] <= x;
+    const int t = (int)__reduce_add_sync(kFull, n) - 1;
+    int rem = (int)(x - before[t]);
+    for (p.b = t * per;; ++p.b) {
+      p.len = seq_len(c, p.b);
+      p.tiles = tiles_in<UNIT>(p.len);
+      const int cost = p.tiles > 0 ? p.tiles + kItemCost : 0;
+      if (rem < cost) break;
+      rem -= cost;
     }
-  }
-  if (threadIdx.x == 0) a.desc[cta] = make_int4(0, 0, -1, 0);
-  if (n_units <= 0) return;
-
-  Cursor cp;
-  {
-    const long long rem = s_rem;
-    cp.b = s_b;
-    cp.len = seq_len(c, cp.b);
-    cp.tiles = (cp.len + kUnit - 1) / kUnit;
-    cp.it = (int)(rem / cp.tiles);
-    cp.tile = (int)(rem - (long long)cp.it * cp.tiles);
-  }
+    p.tile = max(0, rem - kItemCost);
+    p.left = (int)(end - x) - max(0, kItemCost - rem);
+    return p;
+  };
+  const unsigned jobs = (unsigned)ranges * items;
+  Cursor cp = open_job(cta * kWarps + warp);
   Cursor ld = cp;
 
-  // ---- loads: lane r and lane 16 + r own key r of the warp's share --------------
+  // ---- loads: 16-byte chunk `sub` of rows rr, rr + RPI, ... of the unit ---------------
+  constexpr int CH = TL::kRow / 16, RPI = 32 / CH;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES) * TL::kStage;
-  const int kr = lane & 15;
-  auto page_of = [&](const Cursor& p) -> int {  // page of this lane's key, -1: none
-    const int pos = p.tile * kUnit + warp * kKeys + kr;
+  const int sub = lane % CH, rr = lane / CH;
+  constexpr bool SWZ = TL::kSwizzle;
+  static_assert(!SWZ || RPI == 4, "rows 4 i + rr");
+  const uint32_t dst0 = ring + rr * TL::kPitch + (SWZ ? sub ^ rr : sub) * 16;
+  // row i * RPI + rr of a stage's part that starts at `part`
+  auto row_at = [&](uint32_t part, int i) -> uint32_t {
+    return (SWZ && (i & 1) ? part ^ 64 : part) + i * RPI * TL::kPitch;
+  };
+  auto page_index = [&](int pos) { return (int)(((unsigned long long)(unsigned)pos * a.page_mul) >> a.page_shift); };
+  auto at16 = [](const void* base, unsigned long long pieces) { return (const char*)base + (pieces << 4); };
+  // Page of a key, -1: none.  Where 16 divides the page size 16 keys share a page: lane 16 h
+  // holds the h-th sixteen's; else lane r holds key r's (and lane 16 + r too when H = 1).
+  auto page_of = [&](const Cursor& p) -> int {
+    const int pos = p.tile * UNIT + (a.one_page ? (lane >> 4) * (H - 1) * kHalf : lane % UNIT);
     if (pos >= p.len) return -1;
-    const int id = c.block_table[(int64_t)p.b * c.table_stride + pos / c.page_size];
+    const int id = c.block_table[(int64_t)p.b * c.table_stride + page_index(pos)];
     if (id < 0 || id >= c.num_pages) {
       report_error(a.err, ERRBIT_DATA);
       return -1;
@@ -253,65 +325,129 @@ decode_kernel(const __grid_constant__ DecArgs a) {
     return id;
   };
   auto issue = [&](const Cursor& p, int page, int stage) {
-    const uint32_t base = ring + stage * TL::kStage;
-    const int pos = p.tile * kUnit + warp * kKeys + kr;
-    const int off = pos % c.page_size, kvh = p.it / a.mts;
-    const int es = F8 ? 1 : 2;
-    const bool ok = page >= 0;
-    const int64_t pg = ok ? page : 0;
-    const int64_t of = ok ? off : 0;
-    const unsigned mask = __ballot_sync(kFull, ok) & 0xffffu;
-    if (lane == 0) masks[warp][stage] = mask;
-    const bool is_v = lane >= 16;
-    const char* src = (const char*)(is_v ? c.v : c.k) +
-                      (pg * (is_v ? c.v_page_stride : c.k_page_stride) +
-                       of * (is_v ? c.v_token_stride : c.k_token_stride) +
-                       kvh * (is_v ? c.v_head_stride : c.k_head_stride)) * es;
-    if (F8) {
-      const float* sc = (is_v ? c.v_scale : c.k_scale) + (pg * c.page_size + of) * c.kv_heads + kvh;
-      cp_async4(base + TL::kRows + lane * 4, sc, ok ? 4u : 0u);
-    }
-    constexpr int RPI = 32 / TL::kChunks;  // rows per instruction
-    const int sub = lane % TL::kChunks, rr = lane / TL::kChunks;
+    const uint32_t dst = dst0 + stage * TL::kStage;
+    const uint32_t sdst = ring + stage * TL::kStage + TL::kRows + lane * 4;
+    const int pos0 = p.tile * UNIT;
+    const unsigned kvh = a.mts == 1 ? p.it : p.it / a.mts;
+    if (a.one_page) {
+      unsigned mask = 0;
 #pragma unroll
-    for (int i = 0; i < 32 / RPI; ++i) {
-      const int r = i * RPI + rr;  // 0..15: K rows, 16..31: V rows
-      const char* s = (const char*)__shfl_sync(kFull, (unsigned long long)src, r);
-      const uint32_t bytes = (mask >> (r & 15)) & 1u ? 16u : 0u;
-      cp_async16(base + (r >> 4) * (kKeys * TL::kRow) + TL::at(r & 15, sub), s + sub * 16, bytes);
+      for (int h = 0; h < H; ++h) {
+        const int id = H == 1 ? page : __shfl_sync(kFull, page, h * 16);
+        const int first = pos0 + h * kHalf;
+        const int live = id < 0 ? 0 : min(kHalf, p.len - first);
+        mask |= ((1u << live) - 1) << (h * kHalf);
+        const unsigned pg = max(id, 0), off = live > 0 ? first - page_index(first) * c.page_size : 0;
+        // rows behind the last key: a place of the page itself, never read
+        const unsigned r0 = off + min(rr, max(live - 1, 0));
+        const char* ks = at16(c.k, (unsigned long long)pg * a.k_page + ((unsigned long long)r0 * a.k_token + (kvh * (unsigned long long)a.k_head + sub)));
+        const char* vs = at16(c.v, (unsigned long long)pg * a.v_page + ((unsigned long long)r0 * a.v_token + (kvh * (unsigned long long)a.v_head + sub)));
+        const uint32_t d = dst + h * kHalf * TL::kPitch;
+        if (live == kHalf) {
+#pragma unroll
+          for (int i = 0; i < kHalf / RPI; ++i)
+            cp_async16_full(row_at(d, i), at16(ks, (unsigned long long)a.k_token * (i * RPI)));
+#pragma unroll
+          for (int i = 0; i < kHalf / RPI; ++i)
+            cp_async16_full(row_at(d + UNIT * TL::kPitch, i), at16(vs, (unsigned long long)a.v_token * (i * RPI)));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHalf / RPI; ++i) {
+            const bool on = i * RPI + rr < live;
+            cp_async16(row_at(d, i), on ? at16(ks, (unsigned long long)a.k_token * (i * RPI)) : ks, on ? 16u : 0u);
+            cp_async16(row_at(d + UNIT * TL::kPitch, i), on ? at16(vs, (unsigned long long)a.v_token * (i * RPI)) : vs, on ? 16u : 0u);
+          }
+        }
+        if (F8) {
+          const int key = lane % kHalf;
+          const bool on = key < live;
+          const int64_t at = ((int64_t)pg * c.page_size + off + (on ? key : 0)) * c.kv_heads + kvh;
+          // lanes 0-15: the keys' scales, lanes 16-31 the values'
+          cp_async4(ring + stage * TL::kStage + TL::kRows + ((lane >> 4) * UNIT + h * kHalf + key) * 4,
+                    (lane < 16 ? c.k_scale : c.v_scale) + at, on ? 4u : 0u);
+        }
+      }
+      if (lane == 0) masks[warp][stage] = mask;
+    } else {
+      const bool ok = page >= 0;
+      const unsigned mask = __ballot_sync(kFull, ok) & (UNIT == 32 ? kFull : 0xffffu);
+      if (lane == 0) masks[warp][stage] = mask;
+      const int pos = pos0 + lane % UNIT;
+      const unsigned pg = ok ? page : 0, off = ok ? pos - page_index(pos) * c.page_size : 0;
+      const unsigned long long ks = (unsigned long long)pg * a.k_page + (unsigned long long)off * a.k_token + (unsigned long long)kvh * a.k_head;
+      const unsigned long long vs = (unsigned long long)pg * a.v_page + (unsigned long long)off * a.v_token + (unsigned long long)kvh * a.v_head;
+      if (F8) {
+        const int64_t at = ((int64_t)pg * c.page_size + off) * c.kv_heads + kvh;
+        cp_async4(sdst, c.k_scale + at, ok ? 4u : 0u);
+        cp_async4(sdst + UNIT * 4, c.v_scale + at, ok ? 4u : 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < UNIT / RPI; ++i) {
+        const int r = i * RPI + rr;
+        const unsigned bytes = (mask >> r) & 1u ? 16u : 0u;
+        cp_async16(row_at(dst, i), at16(c.k, __shfl_sync(kFull, ks, r) + sub), bytes);
+        cp_async16(row_at(dst + UNIT * TL::kPitch, i), at16(c.v, __shfl_sync(kFull, vs, r) + sub), bytes);
+      }
     }
   };
 
-  int page = page_of(ld);
-  long long loaded = 0;
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) {
-    if (loaded < n_units) {
-      issue(ld, page, s);
-      ++loaded;
-      next_unit(ld, c, items);
-      if (loaded < n_units) page = page_of(ld);
-    }
-    cp_commit();
-  }
-
   uint32_t qf[NT][KS][2];
-  float qs[NT][2];  // F8: factor of this thread's two query columns
+  float qs[NT][2];  // factor of this thread's two query columns
   float m[NT][2], l[NT][2];
   float oacc[NT][KS][4];
   const int tg = lane & 3, gr = lane >> 2;
-  bool fresh = true;
-  int t0 = cp.tile, stage = 0;
+  bool fresh = true, waited = false, more = jobs > (unsigned)W;
+  int stage = 0, into = 0, inflight = 0, t0 = 0;
+  unsigned opened = 0, closed = 0;  // ranges put into and taken out of the fifo
+  int page = ld.left > 0 ? page_of(ld) : -1;
 
-  for (long long i = 0; i < n_units; ++i) {
+  for (;;) {
+    while (inflight < STAGES) {
+      if (ld.left <= 0) {
+        if (!more || opened - closed == kFifo) break;
+        if (!waited) break;
+        unsigned r = 0;
+        if (lane == 0) r = atomicAdd(&a.counts[0], 1u);
+        r = __shfl_sync(kFull, r, 0) + W;
+        more = r < jobs;
+        if (!more) break;
+        ld = open_job(r);
+        if (ld.left <= 0) continue;
+        __syncwarp();  // every lane has read what the place held before
+        if (lane == 0) fifo[warp][opened % kFifo] = ld;
+        ++opened;
+        page = page_of(ld);
+      }
+      issue(ld, page, into);
+      cp_commit();
+      ++inflight;
+      into = into + 1 == STAGES ? 0 : into + 1;
+      next_unit<UNIT>(ld, c);
+      if (ld.left > 0) page = page_of(ld);
+    }
+    if (!waited) {  // from here on: the rows of the slots, and the counts
+      pdl_wait();
+      waited = true;
+      if (cp.left <= 0 && more) continue;
+    }
+    if (cp.left <= 0) {
+      if (opened == closed) break;
+      __syncwarp();
+      cp = fifo[warp][closed++ % kFifo];
+      fresh = true;
+    }
     if (fresh) {  // first unit of an item here
       fresh = false;
       t0 = cp.tile;
       const int mt = cp.it % a.mts, kvh = cp.it / a.mts;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        int head = 0;
-        const int row = query_row(a, cp.b, mt * R + 8 * t + gr, kvh, &head);
+        int head = 0, row = -1;
+        if (mt * R + 8 * t + gr < a.G) {
+          row = query_slot(a, cp.b, mt * R + 8 * t + gr, kvh, &head);
+          if (a.slots) row = a.inv[row];
+          if (row >= c.B * a.kslots) row = -1;
+        }
         const bf16* qr = a.q + (row < 0 ? 0 : (int64_t)row * a.ldq + (int64_t)head * DH);
         float amax = 0.0f;
 #pragma unroll
@@ -357,327 +493,486 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       }
     }
 
-    cp_wait<STAGES - 2>();
-    __syncwarp();
-    const uint32_t base = ring + stage * TL::kStage;
+    if (inflight == STAGES) {
+      cp_wait<STAGES - 1>();
+    } else if (STAGES > 2 && inflight == STAGES - 1) {
+      cp_wait<STAGES - 2>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncwarp();  // every lane's copies and the mask are seen by all
     const unsigned mask = masks[warp][stage];
+    const uint32_t base = ring + stage * TL::kStage;
     if (mask) {
-      float s[NT][4];
+      float s[H][NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[t][j] = 0.0f;
-      float ks0 = 1.0f, ks1 = 1.0f, vs0 = 1.0f, vs1 = 1.0f;
-      if (!F8) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t f[4];
-          ldsm4(f, base + TL::at(((lane >> 3) & 1) * 8 + (lane & 7), 2 * k + (lane >> 4)));
+          for (int j = 0; j < 4; ++j) s[h][t][j] = 0.0f;
+      float ks[H][2], vs[H][2];
+      const uint32_t kb = base + (lane & 15) * TL::kPitch + ((lane >> 4) ^ (SWZ ? lane & 7 : 0)) * 16;
+      auto chunk = [](uint32_t at, int c) -> uint32_t { return SWZ ? at ^ (16 * c) : at + 16 * c; };  // c even
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816<false>(s[t], f, qf[t][k][0], qf[t][k][1]);
-        }
-      } else {
+      for (int h = 0; h < H; ++h) {
+        const uint32_t kh = kb + h * kHalf * TL::kPitch;
+        if (!F8) {
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {  // 32 dims: two 16-byte chunks
-          uint32_t f[4];
-          ldsm4(f, base + TL::at(((lane >> 3) & 1) * 8 + (lane & 7), k + (lane >> 4)));
+          for (int k = 0; k < KS; ++k) {
+            uint32_t f[4];
+            ldsm4(f, chunk(kh, 2 * k));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t g[4];
-            g[0] = e4m3_to_half2((uint16_t)f[2 * h]);
-            g[1] = e4m3_to_half2((uint16_t)f[2 * h + 1]);
-            g[2] = e4m3_to_half2((uint16_t)(f[2 * h] >> 16));
-            g[3] = e4m3_to_half2((uint16_t)(f[2 * h + 1] >> 16));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<true>(s[t], g, qf[t][k + h][0], qf[t][k + h][1]);
+            for (int t = 0; t < NT; ++t) mma16816<false>(s[h][t], f, qf[t][k][0], qf[t][k][1]);
           }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {  // 32 dims: two 16-byte chunks
+            uint32_t f[4];
+            ldsm4(f, chunk(kh, k));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t g[4];
+              g[0] = e4m3_to_half2((uint16_t)f[2 * e]);
+              g[1] = e4m3_to_half2((uint16_t)f[2 * e + 1]);
+              g[2] = e4m3_to_half2((uint16_t)(f[2 * e] >> 16));
+              g[3] = e4m3_to_half2((uint16_t)(f[2 * e + 1] >> 16));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816<true>(s[h][t], g, qf[t][k + e][0], qf[t][k + e][1]);
+            }
+          }
+          const float* sc = reinterpret_cast<const float*>(smem + (size_t)(warp * STAGES + stage) * TL::kStage + TL::kRows) + h * kHalf;
+          ks[h][0] = sc[gr]; ks[h][1] = sc[gr + 8];
+          vs[h][0] = sc[UNIT + gr]; vs[h][1] = sc[UNIT + gr + 8];
         }
-        const float* sc = reinterpret_cast<const float*>(smem + (size_t)(warp * STAGES + stage) * TL::kStage + TL::kRows);
-        ks0 = sc[gr]; ks1 = sc[gr + 8];
-        vs0 = sc[16 + gr]; vs1 = sc[24 + gr];
+      }
+      if (mask != (UNIT == 32 ? kFull : 0xffffu)) {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool on = (mask >> (h * kHalf + 8 * e + gr)) & 1u;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if (!on) s[h][t][2 * e] = s[h][t][2 * e + 1] = -INFINITY;
+            }
+            if (F8 && !on) ks[h][e] = 1.0f;  // a scale that was not copied is 0
+          }
       }
       // The reference m of a query's weights: its largest score; with scaled values the
       // largest score times the value's scale, so that the weights times the scales, which
       // are rounded to fp16 for the second product, are at most 1.
-      const float ls0 = F8 ? fmaxf(log2f(vs0), -100.0f) : 0.0f, ls1 = F8 ? fmaxf(log2f(vs1), -100.0f) : 0.0f;
-      const bool on0 = (mask >> gr) & 1u, on1 = (mask >> (gr + 8)) & 1u;
+      float top[NT][2];
+      bool grows = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        uint32_t pf[2];
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          s[t][j] = on0 ? s[t][j] * qs[t][j] * ks0 : -INFINITY;
-          s[t][2 + j] = on1 ? s[t][2 + j] * qs[t][j] * ks1 : -INFINITY;
-          float top = fmaxf(s[t][j] + ls0, s[t][2 + j] + ls1);
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-          const float mn = fmaxf(m[t][j], top);
-          const float ref = mn == -INFINITY ? 0.0f : mn;
-          const float al = ex2(m[t][j] - ref);
-          m[t][j] = mn;
-          s[t][j] = ex2(s[t][j] - ref);
-          s[t][2 + j] = ex2(s[t][2 + j] - ref);
-          l[t][j] = l[t][j] * al + (s[t][j] + s[t][2 + j]);
+        for (int j = 0; j < 2; ++j) top[t][j] = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            oacc[t][k][j] *= al;
-            oacc[t][k][2 + j] *= al;
-          }
-        }
-        if (F8) {
-          pf[0] = transpose8(pack_f16(s[t][0] * vs0, s[t][1] * vs0));
-          pf[1] = transpose8(pack_f16(s[t][2] * vs1, s[t][3] * vs1));
-        } else {
-          pf[0] = transpose8(pack_bf16(s[t][0], s[t][1]));
-          pf[1] = transpose8(pack_bf16(s[t][2], s[t][3]));
-        }
-        s[t][0] = __uint_as_float(pf[0]);
-        s[t][1] = __uint_as_float(pf[1]);
-      }
-      const uint32_t vb = base + kKeys * TL::kRow;
-      if (!F8) {
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t f[4];
-          ldsm4_t(f, vb + TL::at((lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)));
+        for (int e = 0; e < 2; ++e) {
+          const float ls = F8 ? fmaxf(__log2f(vs[h][e]), -100.0f) : 0.0f;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            mma16816<false>(oacc[t][k], f, __float_as_uint(s[t][0]), __float_as_uint(s[t][1]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float& v = s[h][t][2 * e + j];
+              if (F8) v *= qs[t][j] * ks[h][e];
+              top[t][j] = fmaxf(top[t][j], F8 ? v + ls : v);
+            }
         }
-      } else {
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          // transposed pairs of bytes: keys 2 tg, 2 tg + 1 of dims 2 gr, 2 gr + 1
-          uint32_t f[4];
-          ldsm4_t(f, vb + TL::at(((lane >> 3) & 1) * 8 + (lane & 7), k + (lane >> 4)));
+      for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t g[4];  // rows gr: even dims, rows gr + 8: odd dims
-            const uint32_t lo = f[2 * h], hi = f[2 * h + 1];
-            g[0] = e4m3_to_half2((uint16_t)__byte_perm(lo, 0, 0x0020));
-            g[1] = e4m3_to_half2((uint16_t)__byte_perm(lo, 0, 0x0031));
-            g[2] = e4m3_to_half2((uint16_t)__byte_perm(hi, 0, 0x0020));
-            g[3] = e4m3_to_half2((uint16_t)__byte_perm(hi, 0, 0x0031));
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-              mma16816<true>(oacc[t][k + h], g, __float_as_uint(s[t][0]), __float_as_uint(s[t][1]));
-          }
-        }
-      }
-    }
-    __syncwarp();  // the stage before this one is free: every lane has read it
-    if (loaded < n_units) {
-      issue(ld, page, stage == 0 ? STAGES - 1 : stage - 1);
-      ++loaded;
-      next_unit(ld, c, items);
-      if (loaded < n_units) page = page_of(ld);
-    }
-    cp_commit();
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-
-    const bool ends = cp.tile + 1 == cp.tiles;
-    if (ends || i + 1 == n_units) {
-      // ---- join the four warps --------------------------------------------------
+          for (int j = 0; j < 2; ++j) top[t][j] = fmaxf(top[t][j], __shfl_xor_sync(kFull, top[t][j], off));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float v = l[t][j];
-          v += __shfl_xor_sync(kFull, v, 4);
-          v += __shfl_xor_sync(kFull, v, 8);
-          v += __shfl_xor_sync(kFull, v, 16);
-          l[t][j] = v;
-          if (lane < 4) {
-            mls[(warp * R + 8 * t + 2 * tg + j) * 2] = m[t][j];
-            mls[(warp * R + 8 * t + 2 * tg + j) * 2 + 1] = v;
+          if (!F8) top[t][j] *= qs[t][j];
+          grows |= top[t][j] > m[t][j];
+        }
+      if (__any_sync(kFull, grows)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float mn = fmaxf(top[t][j], m[t][j]);
+            const float al = m[t][j] == -INFINITY ? 0.0f : ex2(m[t][j] - mn);
+            m[t][j] = mn;
+            l[t][j] *= al;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              oacc[t][k][j] *= al;
+              oacc[t][k][2 + j] *= al;
+            }
+          }
+      }
+      float ref[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ref[t][j] = m[t][j] == -INFINITY ? 0.0f : m[t][j];
+      const uint32_t vb = base + UNIT * TL::kPitch;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float* w = s[h][t];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            w[j] = ex2(F8 ? w[j] - ref[t][j] : fmaf(w[j], qs[t][j], -ref[t][j]));
+            w[2 + j] = ex2(F8 ? w[2 + j] - ref[t][j] : fmaf(w[2 + j], qs[t][j], -ref[t][j]));
+            l[t][j] += w[j] + w[2 + j];
+          }
+          if (F8) {
+            pf[t][0] = transpose8(pack_f16(w[0] * vs[h][0], w[1] * vs[h][0]));
+            pf[t][1] = transpose8(pack_f16(w[2] * vs[h][1], w[3] * vs[h][1]));
+          } else {
+            pf[t][0] = transpose8(pack_bf16(w[0], w[1]));
+            pf[t][1] = transpose8(pack_bf16(w[2], w[3]));
           }
         }
-      __syncthreads();
+        const uint32_t vh = vb + h * kHalf * TL::kPitch;
+        if (!F8) {
+          const uint32_t va = vh + ((lane >> 4) * 8 + (lane & 7)) * TL::kPitch +
+                              (((lane >> 3) & 1) ^ (SWZ ? lane & 7 : 0)) * 16;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t f[4];
+            ldsm4_t(f, chunk(va, 2 * k));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816<false>(oacc[t][k], f, pf[t][0], pf[t][1]);
+          }
+        } else {
+          const uint32_t va = vh + (lane & 15) * TL::kPitch + ((lane >> 4) ^ (SWZ ? lane & 7 : 0)) * 16;
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            // transposed pairs of bytes: keys 2 tg, 2 tg + 1 of dims 2 gr, 2 gr + 1
+            uint32_t f[4];
+            ldsm4_t(f, chunk(va, k));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t g[4];  // rows gr: even dims, rows gr + 8: odd dims
+              const uint32_t e0 = __byte_perm(f[2 * e], 0, 0x3120), e1 = __byte_perm(f[2 * e + 1], 0, 0x3120);
+              g[0] = e4m3_to_half2((uint16_t)e0);
+              g[1] = e4m3_to_half2((uint16_t)(e0 >> 16));
+              g[2] = e4m3_to_half2((uint16_t)e1);
+              g[3] = e4m3_to_half2((uint16_t)(e1 >> 16));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816<true>(oacc[t][k + e], g, pf[t][0], pf[t][1]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage is free: every lane has read it
+    --inflight;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+
+    const bool ends = cp.tile + 1 == cp.tiles;
+    if (ends || cp.left <= 1) {
+      // ---- the item ends, or its part in this range ----------------------------------
+      const int mt = cp.it % a.mts, kvh = cp.it / a.mts;
+      const bool whole = ends && t0 == 0;
+      const int pitch = min(R, a.G), slot = t0 > 0 ? 0 : 1;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int n = 8 * t + 2 * tg + j;
-          float top = -INFINITY;
+          float v = l[t][j];
+          v += __shfl_xor_sync(kFull, v, 4);
+          v += __shfl_xor_sync(kFull, v, 8);
+          v += __shfl_xor_sync(kFull, v, 16);
+          if (mt * R + n >= a.G) continue;
+          if (whole) {
+            const int place = query_place(a, cp.b, mt * R + n, kvh);
+            if (place < 0) continue;
+            const float inv = v == 0.0f ? 0.0f : 1.0f / v;
+            bf16* o = a.o + (int64_t)place * DH;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mls[(w * R + n) * 2]);
-          const float f = top == -INFINITY ? 0.0f : ex2(m[t][j] - top);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            oacc[t][k][j] *= f;
-            oacc[t][k][2 + j] *= f;
-          }
-        }
-      for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int dim = 16 * k + (F8 ? 2 * gr + (j >> 1) : gr + 8 * (j >> 1));
-                float* d = red + (8 * t + 2 * tg + (j & 1)) * RED + dim;
-                *d = (w == 0 ? 0.0f : *d) + oacc[t][k][j];
+            for (int k = 0; k < KS; ++k) {
+              const float e0 = oacc[t][k][j] * inv, e1 = oacc[t][k][2 + j] * inv;
+              if (F8) {
+                *reinterpret_cast<uint32_t*>(o + 16 * k + 2 * gr) = pack_bf16(e0, e1);
+              } else {
+                o[16 * k + gr] = __float2bfloat16_rn(e0);
+                o[16 * k + gr + 8] = __float2bfloat16_rn(e1);
               }
-        }
-        __syncthreads();
-      }
-      const int mt = cp.it % a.mts, kvh = cp.it / a.mts;
-      const bool whole = t0 == 0 && ends;
-      const int slot = t0 > 0 ? 0 : 1;  // 0: an item started before, 1: one that goes on after
-      for (int e = threadIdx.x; e < R * (DH / 8); e += kThreads) {
-        const int n = e / (DH / 8), d0 = 8 * (e % (DH / 8));
-        if (mt * R + n >= a.G) continue;
-        float top = -INFINITY, sum = 0.0f;
+            }
+            if (a.lse && gr == 0)
+              a.lse[place] = v == 0.0f ? -INFINITY : (log2f(v) + m[t][j]) * 0.6931471805599453f;
+          } else {
+            const int64_t at = (((int64_t)cp.range * items + cp.it) * 2 + slot) * pitch + n;
+            float* po = a.part_o + at * DH;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mls[(w * R + n) * 2]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = mls[(w * R + n) * 2];
-          if (mw != -INFINITY) sum += mls[(w * R + n) * 2 + 1] * ex2(mw - top);
-        }
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = red[n * RED + d0 + j];
-        if (whole) {
-          int head;
-          const int row = query_row(a, cp.b, mt * R + n, kvh, &head);
-          if (row < 0) continue;
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= inv;
-          const int64_t at = (int64_t)row * a.q_heads + head;
-          *reinterpret_cast<uint4*>(a.o + at * DH + d0) = pack8(v);
-          if (a.lse && d0 == 0)
-            a.lse[at] = sum == 0.0f ? -INFINITY : (log2f(sum) + top) * 0.6931471805599453f;
-        } else {
-          const int64_t at = ((int64_t)cta * 2 + slot) * R + n;
-          float* po = a.part_o + at * DH + d0;
-          *reinterpret_cast<float4*>(po) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(po + 4) = make_float4(v[4], v[5], v[6], v[7]);
-          if (d0 == 0) {
-            a.part_ml[at * 2] = top;
-            a.part_ml[at * 2 + 1] = sum;
+            for (int k = 0; k < KS; ++k) {
+              if (F8) {
+                *reinterpret_cast<float2*>(po + 16 * k + 2 * gr) = make_float2(oacc[t][k][j], oacc[t][k][2 + j]);
+              } else {
+                po[16 * k + gr] = oacc[t][k][j];
+                po[16 * k + gr + 8] = oacc[t][k][2 + j];
+              }
+            }
+            if (gr == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m[t][j], v);
           }
         }
+      if (slot == 1 && !whole && lane == 0) {
+        const long long here = min(total, start_of(cp.range + 1)) - cp.left;
+        a.split[atomicAdd(&a.counts[1], 1u)] =
+            make_int4(cp.b, cp.it, cp.range, range_of(here + cp.tiles - 1 - cp.tile));
       }
-      if (slot == 1 && !whole && threadIdx.x == 0) {
-        // the CTA that holds the item's last unit: the one whose run contains it
-        const long long last = u0 + i + (cp.tiles - 1 - cp.tile);
-        a.desc[cta] = make_int4(cp.b, cp.it, (int)(((last + 1) * ctas - 1) / U), 0);
-      }
-      __syncthreads();
       fresh = true;
     }
-    next_unit(cp, c, items);
+    next_unit<UNIT>(cp, c);
   }
+  // sequences without a cached token: o = 0, lse = -inf
+  for (int b = cta; b < c.B; b += gridDim.x) {
+    if (seq_len(c, b) > 0) continue;
+    for (int i = threadIdx.x; i < a.G * c.kv_heads * (DH / 8); i += kThreads) {
+      const int place = query_place(a, b, i / (DH / 8) % a.G, i / (DH / 8) / a.G);
+      if (place < 0) continue;
+      *reinterpret_cast<uint4*>(a.o + (int64_t)place * DH + 8 * (i % (DH / 8))) = make_uint4(0, 0, 0, 0);
+      if (a.lse && i % (DH / 8) == 0) a.lse[place] = -INFINITY;
+    }
+  }
+  pdl_trigger();
   cp_wait<0>();
 }
 
-// Joins the shares of the items that several CTAs hold: block c the item that CTA c
-// started, from its second slot and the first slots of the CTAs after it, in order.
+// Joins the shares of the items that several ranges hold, row by row (of 8 NT a query
+// tile): the share of the range that started the item, then those of the ranges after it.
+// A warp takes a row with up to kFew shares, else the CTA's warps take every kJoinWarps-th
+// share each and their sums are joined in order.
+constexpr int kJoinWarps = 8, kFew = 24;
+
 template <int DH>
-__global__ void __launch_bounds__(256)
-decode_join_kernel(const __grid_constant__ DecArgs a, int R) {
-  const int cta = blockIdx.x;
-  const int4 d = a.desc[cta];
-  if (d.z < 0) return;
-  const int mt = d.y % a.mts, kvh = d.y / a.mts;
-  for (int e = threadIdx.x; e < R * (DH / 4); e += 256) {
-    const int n = e / (DH / 4), d0 = 4 * (e % (DH / 4));
-    int head;
-    const int row = query_row(a, d.x, mt * R + n, kvh, &head);
-    if (row < 0) continue;
-    float top = -INFINITY;
-    for (int j = cta; j <= d.z; ++j)
-      top = fmaxf(top, a.part_ml[(((int64_t)j * 2 + (j == cta)) * R + n) * 2]);
-    float sum = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (top != -INFINITY) {
-      for (int j = cta; j <= d.z; ++j) {
-        const int64_t at = ((int64_t)j * 2 + (j == cta)) * R + n;
-        const float f = ex2(a.part_ml[at * 2] - top);
-        sum += f * a.part_ml[at * 2 + 1];
-        const float4 p = *reinterpret_cast<const float4*>(a.part_o + at * DH + d0);
-        v.x += f * p.x; v.y += f * p.y; v.z += f * p.z; v.w += f * p.w;
+struct Joined {
+  float top, sum, v[DH / 32];  // value 32 k + lane
+};
+template <int DH>
+__device__ __forceinline__ Joined<DH> join_shares(const DecArgs& a, int it, int first, int last, int n, int pitch,
+                                                  int from, int step, int lane) {
+  constexpr int N = DH / 32, kAhead = 8;
+  const int items = a.c.kv_heads * a.mts;
+  Joined<DH> r;
+  r.top = -INFINITY;
+  r.sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) r.v[k] = 0.0f;
+  for (int j0 = first + from; j0 <= last; j0 += step * kAhead) {
+    float2 s[kAhead];
+    float p[kAhead][N];
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h) {
+      const int j = j0 + h * step;
+      s[h] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) p[h][k] = 0.0f;
+      if (j <= last) {
+        const int64_t at = (((int64_t)j * items + it) * 2 + (j == first)) * pitch + n;
+        s[h] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+#pragma unroll
+        for (int k = 0; k < N; ++k) p[h][k] = a.part_o[at * DH + 32 * k + lane];
       }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = (int64_t)row * a.q_heads + head;
-    uint2 out;
-    out.x = pack_bf16(v.x * inv, v.y * inv);
-    out.y = pack_bf16(v.z * inv, v.w * inv);
-    *reinterpret_cast<uint2*>(a.o + at * DH + d0) = out;
-    if (a.lse && d0 == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (log2f(sum) + top) * 0.6931471805599453f;
+    float up = r.top;
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h) up = fmaxf(up, s[h].x);
+    if (up == -INFINITY) continue;
+    const float al = r.top == -INFINITY ? 0.0f : ex2(r.top - up);
+    r.top = up;
+    r.sum *= al;
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.v[k] *= al;
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h) {
+      const float f = s[h].x == -INFINITY ? 0.0f : ex2(s[h].x - up);
+      r.sum += f * s[h].y;
+#pragma unroll
+      for (int k = 0; k < N; ++k) r.v[k] += f * p[h][k];
+    }
+  }
+  return r;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+decode_join_kernel(const __grid_constant__ DecArgs a, int R) {
+  constexpr int N = DH / 32;
+  __shared__ float2 ml[kJoinWarps];
+  __shared__ float sums[kJoinWarps][DH];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pitch = min(R, a.G);
+  pdl_wait();
+  const int all = (int)a.counts[1] * pitch, step = kJoinWarps * gridDim.x;
+  bool many = false;
+  for (int u = warp * gridDim.x + blockIdx.x; u < all; u += step) {
+    const int4 d = a.split[u / pitch];
+    const int n = u % pitch, mt = d.y % a.mts, kvh = d.y / a.mts;
+    if (mt * R + n >= a.G) continue;
+    if (d.w - d.z >= kFew) {
+      many = true;
+      continue;
+    }
+    const int place = query_place(a, d.x, mt * R + n, kvh);
+    const Joined<DH> r = join_shares<DH>(a, d.y, d.z, d.w, n, pitch, 0, 1, lane);
+    const float inv = r.sum == 0.0f ? 0.0f : 1.0f / r.sum;
+    if (place < 0) continue;
+#pragma unroll
+    for (int k = 0; k < N; ++k) a.o[(int64_t)place * DH + 32 * k + lane] = __float2bfloat16_rn(r.v[k] * inv);
+    if (a.lse && lane == 0)
+      a.lse[place] = r.sum == 0.0f ? -INFINITY : (log2f(r.sum) + r.top) * 0.6931471805599453f;
+  }
+  if (!__syncthreads_or(many)) return;
+  for (int u = blockIdx.x; u < all; u += gridDim.x) {
+    const int4 d = a.split[u / pitch];
+    const int n = u % pitch, mt = d.y % a.mts, kvh = d.y / a.mts;
+    if (d.w - d.z < kFew || mt * R + n >= a.G) continue;
+    const Joined<DH> r = join_shares<DH>(a, d.y, d.z, d.w, n, pitch, warp, kJoinWarps, lane);
+    if (lane == 0) ml[warp] = make_float2(r.top, r.sum);
+#pragma unroll
+    for (int k = 0; k < N; ++k) sums[warp][32 * k + lane] = r.v[k];
+    __syncthreads();
+    if (threadIdx.x < DH) {
+      float top = -INFINITY, sum = 0.0f, v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, ml[w].x);
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ml[w].x == -INFINITY ? 0.0f : ex2(ml[w].x - top);
+        sum += f * ml[w].y;
+        v += f * sums[w][threadIdx.x];
+      }
+      const int place = query_place(a, d.x, mt * R + n, kvh);
+      if (place >= 0) {
+        a.o[(int64_t)place * DH + threadIdx.x] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : v / sum);
+        if (a.lse && threadIdx.x == 0)
+          a.lse[place] = sum == 0.0f ? -INFINITY : (log2f(sum) + top) * 0.6931471805599453f;
+      }
+    }
+    __syncthreads();
   }
 }
 
 // Query tiles: 8 columns of the product for each 8 of the G rows, up to 32 in one pass
 // over the keys.
-int tiles_of(int G) { return G <= 8 ? 1 : G <= 16 ? 2 : 4; }
-// CTAs: a fixed count, so that the split (and the workspace) is the same on any GPU;
-// two on each of 148 SMs, one where 32 queries fill the registers.
-int ctas_of(int NT) { return NT == 4 ? 148 : 296; }
+int tiles_of(int G) { return G <= 8 ? 1 : G <= 16 ? 2 : G <= 24 ? 3 : 4; }
+
+// CTAs on each of 148 SMs: three where the registers allow it (8 queries), else two.
+int workers_of(int nt) { return 148 * kWarps * (nt == 1 ? 3 : 2); }
+
+// Starts while the kernel before it still runs, and waits for it on the device.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 template <int DH, int NT, bool F8>
 cudaError_t run(const DecArgs& a, cudaStream_t s) {
   using TL = Tile<DH, F8>;
-  constexpr int most = NT == 4 ? 49152 : 24576;  // ring bytes of a warp
-  constexpr int STAGES = most / TL::kStage > 6 ? 6 : most / TL::kStage;
-  static_assert(STAGES >= 3, "a ring needs three stages");
-  constexpr int R = 8 * NT;
-  constexpr size_t smem = (size_t)kWarps * STAGES * TL::kStage + (size_t)R * (DH + 4) * 4 +
-                          (size_t)kWarps * R * 2 * 4;
-  auto kern = decode_kernel<DH, NT, F8, STAGES>;
+  constexpr int PER_SM = NT == 1 ? 3 : 2;
+  constexpr int kRing = (228 * 1024 / PER_SM - 3584) / (kWarps * TL::kStage);
+  constexpr int STAGES = kRing > 4 ? 4 : kRing;
+  static_assert(STAGES >= 2, "a ring needs two stages");
+  constexpr size_t smem = (size_t)kWarps * STAGES * TL::kStage;
+  auto kern = decode_kernel<DH, NT, F8, STAGES, PER_SM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int grid = ctas_of(NT);
-  kern<<<grid, kThreads, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  decode_join_kernel<DH><<<grid, 256, 0, s>>>(a, R);
-  return cudaGetLastError();
+  if (e == cudaSuccess) e = launch_early(kern, 148 * PER_SM, kThreads, smem, s, a);
+  if (e == cudaSuccess) e = launch_early(decode_join_kernel<DH>, 296, 32 * kJoinWarps, 0, s, a, 8 * NT);
+  return e;
 }
 template <int DH, bool F8>
 cudaError_t run_nt(const DecArgs& a, cudaStream_t s) {
   switch (tiles_of(a.G)) {
     case 1: return run<DH, 1, F8>(a, s);
     case 2: return run<DH, 2, F8>(a, s);
+    case 3: return run<DH, 3, F8>(a, s);
     default: return run<DH, 4, F8>(a, s);
   }
 }
 
+struct DecWorkspace {
+  int workers;
+  size_t part_o, part_ml, split, counts, inv, bytes;
+  DecWorkspace(int rows, int kv_heads, int G, int head_dim) {
+    const int nt = tiles_of(G), items = kv_heads * cdiv(G, 8 * nt);
+    workers = workers_of(nt);
+    const size_t jobs = (size_t)2 * (workers > items ? workers : items);
+    const size_t share_rows = jobs * 2 * (G < 8 * nt ? G : 8 * nt);
+    part_o = 0;
+    part_ml = part_o + share_rows * head_dim * 4;
+    split = (part_ml + share_rows * 2 * 4 + 15) / 16 * 16;
+    counts = split + jobs * sizeof(int4);
+    inv = counts + 16;
+    bytes = inv + (size_t)rows * 4;
+  }
+};
+
 }  // namespace
 
-size_t decode_workspace_bytes(int G, int head_dim) {
-  const int nt = tiles_of(G), R = 8 * nt;
-  const size_t slots = (size_t)ctas_of(nt) * 2 * R;
-  return slots * head_dim * 4 + slots * 2 * 4 + (size_t)ctas_of(nt) * sizeof(int4);
+size_t decode_workspace_bytes(int rows, int kv_heads, int G, int head_dim) {
+  return DecWorkspace(rows, kv_heads, G, head_dim).bytes;
 }
 
-cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, const int32_t* inv,
+cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, const int32_t* sorted_slot,
                           int kslots, int q_heads, void* o, float* lse, void* ws, unsigned* err,
                           cudaStream_t s) {
   DecArgs a;
   a.q = (const bf16*)q;
   a.ldq = ldq;
-  a.inv = inv;
+  a.slots = sorted_slot;
   a.c = c;
   a.kslots = kslots;
   a.q_heads = q_heads;
   a.group = q_heads / c.kv_heads;
   a.G = kslots * a.group;
-  const int nt = tiles_of(a.G), R = 8 * nt;
-  a.mts = cdiv(a.G, R);
+  const int rows = c.B * kslots;
+  a.mts = cdiv(a.G, 8 * tiles_of(a.G));
+  // exact for positions below 2^31: 2^(31 + n) / page_size rounded up, 2^n >= page_size
+  int n = 0;
+  while ((1ll << n) < c.page_size) ++n;
+  a.page_shift = 31 + n;
+  a.page_mul = ((1ull << a.page_shift) + c.page_size - 1) / c.page_size;
+  a.one_page = c.page_size % kHalf == 0;
+  const int es = c.k_scale ? 1 : 2;
+  a.k_page = (unsigned)(c.k_page_stride * es / 16);
+  a.k_token = (unsigned)(c.k_token_stride * es / 16);
+  a.k_head = (unsigned)(c.k_head_stride * es / 16);
+  a.v_page = (unsigned)(c.v_page_stride * es / 16);
+  a.v_token = (unsigned)(c.v_token_stride * es / 16);
+  a.v_head = (unsigned)(c.v_head_stride * es / 16);
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)c.head_dim));
   a.o = (bf16*)o;
   a.lse = lse;
-  const size_t slots = (size_t)ctas_of(nt) * 2 * R;
-  a.part_o = (float*)ws;
-  a.part_ml = a.part_o + slots * c.head_dim;
-  a.desc = (int4*)(a.part_ml + slots * 2);
+  const DecWorkspace w(rows, c.kv_heads, a.G, c.head_dim);
+  char* base = (char*)ws;
+  a.part_o = (float*)(base + w.part_o);
+  a.part_ml = (float*)(base + w.part_ml);
+  a.workers = w.workers;
+  a.split = (int4*)(base + w.split);
+  a.counts = (unsigned*)(base + w.counts);
+  a.inv = (int32_t*)(base + w.inv);
   a.err = err;
+  decode_prepare_kernel<<<cdiv(sorted_slot ? rows : 1, 256), 256, 0, s>>>(sorted_slot, rows, (int32_t*)a.inv,
+                                                                          a.counts, err);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   if (c.k_scale)
     return c.head_dim == 64 ? run_nt<64, true>(a, s) : run_nt<128, true>(a, s);
   return c.head_dim == 64 ? run_nt<64, false>(a, s) : run_nt<128, false>(a, s);

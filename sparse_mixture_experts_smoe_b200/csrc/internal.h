@@ -194,11 +194,12 @@ cudaError_t launch_qk_fwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStre
 cudaError_t launch_qk_bwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s);
 cudaError_t launch_cache_append(const QkArgs& a, cudaStream_t s);
 
-// Paged decode attention (decode.cu).  inv: grouped row of each slot (null: row = slot).
-size_t decode_workspace_bytes(int G, int head_dim);
-cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, const int32_t* inv,
-                          int kslots, int q_heads, void* o, float* lse, void* ws, unsigned* err,
-                          cudaStream_t s);
+// Paged decode attention (decode.cu) of rows = B * kslots grouped rows (sorted_slot null:
+// row = slot), G = queries that share a key head.
+size_t decode_workspace_bytes(int rows, int kv_heads, int G, int head_dim);
+cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c,
+                          const int32_t* sorted_slot, int kslots, int q_heads, void* o, float* lse,
+                          void* ws, unsigned* err, cudaStream_t s);
 
 // e4m3 quantisation (fp8.cu): rows of a bf16 [rows, cols] matrix with one scale per
 // row; weights [E, K, N] bf16 -> codes [E, N, K] with one scale per (e, column)
