@@ -6,9 +6,13 @@
 //   best k of c_e, inside the best top_groups groups when there are groups
 //   gate = scale * s_e, or scale * s_e / (sum of the selected s)
 //
-// Selected ids are whole numbers: they are those of scores compared in 64 bits, ties
-// to the lower id.
+// Selected ids are whole numbers: they are those of scores compared in 64 bits, ties to
+// the lower id.  One warp has a row.  It ranks in 32 bits with scores whose error is
+// bounded, and where two ranks that decide the outcome lie closer together than that
+// bound (and are not equal because logit and bias are), it ranks the row again in 64 bits.
+// Logits of a normal distribution bring that about in under one row of a hundred.
 #include <cfloat>
+#include <climits>
 
 #include "common.cuh"
 
@@ -22,6 +26,50 @@ __device__ __forceinline__ double warp_max64(double v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, off));
   return v;
+}
+// Largest value of the warp; NaN is no value.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_min(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two scores of one row that differ by more than kApart (1 + |c|) rank as in 64 bits.
+// ex2 and rcp are within 2^-22 and 2^-23 of their value and an exponent x loses 2^-23 |x|,
+// which times exp(-|x|) stays under 2^-23: a sigmoid is within 2^-22.  A softmax's sum of
+// up to 1024 terms (32 in a lane, 5 steps across) adds 2^-18.5 of a score, or of the sum of
+// a group's two best, which is at most 1.  So two such values are within 2^-17.5 of their
+// distance, and a bias added to each costs 2^-23 |c| more.
+constexpr float kApart = 1.0f / (1 << 17);
+__device__ __forceinline__ bool apart(float hi, float lo, float size) {
+  return hi - lo > kApart * (1.0f + size);
+}
+
+// The lane that holds the warp's largest (v, then lowest e) of 64-bit values; e < 0: none.
+__device__ __forceinline__ int best_lane64(double v, int e) {
+  long long k = __double_as_longlong(v + 0.0);  // -0 is 0
+  k ^= (k >> 63) & 0x7fffffffffffffffll;        // integer order
+  const int hi = e < 0 ? INT_MIN : (int)(k >> 32);
+  const int top = __reduce_max_sync(kFull, hi);
+  bool in = e >= 0 && hi == top;
+  const unsigned low = __reduce_max_sync(kFull, in ? (unsigned)k : 0u);
+  in = in && (unsigned)k == low;
+  const unsigned first = __reduce_min_sync(kFull, in ? (unsigned)e : 0xffffffffu);
+  return __ffs(__ballot_sync(kFull, in && (unsigned)e == first)) - 1;
 }
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
@@ -88,35 +136,29 @@ __device__ int select_row64(const T* __restrict__ row, const SelectArgs& a, doub
       int bi = -1;
       for (int g = lane; g < a.groups; g += 32)
         if (!((open >> g) & 1ull) && (bi < 0 || gs[g] > bv)) { bv = gs[g]; bi = g; }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        const double ov = __shfl_xor_sync(kFull, bv, off);
-        const int oi = __shfl_xor_sync(kFull, bi, off);
-        if (oi >= 0 && (bi < 0 || ov > bv || (ov == bv && oi < bi))) { bv = ov; bi = oi; }
-      }
-      open |= 1ull << bi;
+      open |= 1ull << __shfl_sync(kFull, bi, best_lane64(bv, bi));
     }
   }
   unsigned taken = 0;  // bit i: expert lane + 32 i is taken
-  int mine = -1;
+  int mine = -1, bi = -1;
+  double bv = 0.0;
+  bool stale = true;
   for (int j = 0; j < a.k; ++j) {
-    double bv = 0.0;
-    int bi = -1;
-    for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
-      if ((taken >> i) & 1u) continue;
-      if (a.groups > 1 && !((open >> (e / n)) & 1ull)) continue;
-      double c = sc[e];
-      if (!a.bias && c > -INFINITY) c = (double)finite_top(to_f(row[e]));  // the order of the logits
-      if (bi < 0 || c > bv) { bv = c; bi = e; }
+    if (stale) {  // this lane's best expert that is left
+      bi = -1;
+      for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
+        if ((taken >> i) & 1u) continue;
+        if (a.groups > 1 && !((open >> (e / n)) & 1ull)) continue;
+        double c = sc[e];
+        if (!a.bias && c > -INFINITY) c = (double)finite_top(to_f(row[e]));  // the order of the logits
+        if (bi < 0 || c > bv) { bv = c; bi = e; }
+      }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const double ov = __shfl_xor_sync(kFull, bv, off);
-      const int oi = __shfl_xor_sync(kFull, bi, off);
-      if (oi >= 0 && (bi < 0 || ov > bv || (ov == bv && oi < bi))) { bv = ov; bi = oi; }
-    }
-    if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-    if (lane == j) mine = bi;
+    __syncwarp();
+    const int src = best_lane64(bv, bi), e = __shfl_sync(kFull, bi, src);
+    stale = lane == src;
+    if (stale) taken |= 1u << (e >> 5);
+    if (lane == j) mine = e;
   }
   __syncwarp();
   return mine;
@@ -150,25 +192,163 @@ __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b,
   return w > 0.0f ? a.scale * (w / sum) : 0.0f;
 }
 
-template <typename T>
+// One row in 32 bits.  The experts of a group lie in `lpg` lanes (a power of two, one
+// group: the warp), C <= NV neighbours in a lane, so that a group's best are found in
+// log2(lpg) steps and lanes are in the order of the ids.  Returns as select_row64; -2 in
+// every lane if two ranks lie too close together.
+template <typename T, int NV>
+__device__ int select_row32(const T* __restrict__ row, const SelectArgs& a, int lpg, int C, int lane,
+                            float* row_max, float* row_den) {
+  const bool soft = a.score == SMOE_SCORE_SOFTMAX;
+  const int n = a.E / a.groups, group = lane / lpg, in0 = (lane & (lpg - 1)) * C;
+  const int e0 = group * n + in0;
+  const int have = group < a.groups ? min(C, n - in0) : 0;  // this lane's experts
+  float l[NV], c[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
+  constexpr int VB = NV * sizeof(T) < 16 ? NV * sizeof(T) : 16;  // bytes of a wide load
+  constexpr int VE = VB / sizeof(T);
+  if (VE > 1 && C == NV && have == NV && ((a.ld | e0) & (VE - 1)) == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; i += VE) {
+      T w[VE];
+      if (VB == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(row + e0 + i);
+      if (VB == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(row + e0 + i);
+      if (VB == 4) *reinterpret_cast<unsigned*>(w) = *reinterpret_cast<const unsigned*>(row + e0 + i);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) l[i + j] = to_f(w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i < have) l[i] = to_f(row[e0 + i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) l[i] = usable(l[i]) ? finite_top(l[i]) : -INFINITY;
+  float mx = 0.0f, den = 1.0f;
+  if (soft && (a.bias || a.groups > 1 || !a.renorm)) {
+    mx = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) mx = fmaxf(mx, l[i]);
+    mx = warp_max(mx);
+    den = 0.0f;
+    if (mx > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) den += ex2((l[i] - mx) * 1.4426950408889634f);
+    }
+    den = warp_sum(den);
+    *row_max = mx;
+    *row_den = den;
+  }
+  // scores, with the bias; without one what is ranked in the end is the logits
+  if (a.bias || a.groups > 1) {
+    const float inv = rcp(den);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float s = soft ? ex2((l[i] - mx) * 1.4426950408889634f) * inv
+                           : rcp(1.0f + ex2(l[i] * -1.4426950408889634f));
+      const float b = a.bias && i < have ? a.bias[e0 + i] : 0.0f;
+      c[i] = l[i] > -INFINITY && b > -INFINITY ? s + b : -INFINITY;
+    }
+  }
+  bool open = group < a.groups, close_by = false;
+  if (a.groups > 1) {
+    float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v2 = fmaxf(v2, fminf(v1, c[i]));
+      v1 = fmaxf(v1, c[i]);
+    }
+    for (int off = 1; off < lpg; off <<= 1) {
+      const float o1 = __shfl_xor_sync(kFull, v1, off), o2 = __shfl_xor_sync(kFull, v2, off);
+      v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
+      v1 = fmaxf(v1, o1);
+    }
+    const float gs = a.group_top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
+    int ahead = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float o = __shfl_sync(kFull, gs, g * lpg);
+      ahead += o > gs || (o == gs && g < group);
+    }
+    const bool there = open;
+    open = open && ahead < a.top_groups;
+    if (a.top_groups < a.groups) {
+      const float in = warp_min(open ? gs : INFINITY), out = warp_max(there && !open ? gs : -INFINITY);
+      const float size = fmaxf(fabsf(v1), v2 > -INFINITY ? fabsf(v2) : 0.0f);
+      close_by = out > -INFINITY && !apart(in, out, warp_max(there && v1 > -INFINITY ? size : 0.0f));
+    }
+  }
+  // unavailable experts rank at -inf, what is not to be chosen is NaN
+  float best = NAN;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (!a.bias) c[i] = l[i];
+    if (!open || i >= have) c[i] = NAN;
+    best = fmaxf(best, c[i]);
+  }
+  const int rounds = a.bias ? a.k + 1 : a.k;  // with scores the next one too, to be compared
+  int mine = -1;
+  float rank = NAN;
+  for (int j = 0; j < rounds; ++j) {
+    const float top = warp_max(best);
+    const unsigned who = __ballot_sync(kFull, best == top);
+    if (who == 0) break;  // no candidate left (only after the k-th)
+    const int src = __ffs(who) - 1;
+    int e = 0;
+    if (lane == src) {
+      bool found = false;
+      best = NAN;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!found && c[i] == top) {
+          found = true;
+          e = e0 + i;
+          c[i] = NAN;
+        }
+        best = fmaxf(best, c[i]);
+      }
+    }
+    e = __shfl_sync(kFull, e, src);
+    if (lane == j) {
+      mine = e;
+      rank = top;
+    }
+  }
+  if (a.bias) {
+    const float next = __shfl_down_sync(kFull, rank, 1);
+    float lm = 0.0f, bm = 0.0f;
+    if (mine >= 0) {
+      lm = finite_top(to_f(row[mine]));
+      bm = a.bias[mine];
+    }
+    const float ln = __shfl_down_sync(kFull, lm, 1), bn = __shfl_down_sync(kFull, bm, 1);
+    // (a NaN: there is no next one)
+    if (lane < a.k && next > -INFINITY && !apart(rank, next, fabsf(rank)) && !(lm == ln && bm == bn)) close_by = true;
+  }
+  if (__any_sync(kFull, close_by)) return -2;
+  return lane < a.k ? mine : -1;
+}
+
+// One warp per row; lpg = 0: every row in 64 bits.
+template <typename T, int NV>
 __global__ void __launch_bounds__(kWarps * 32)
-select64_kernel(const T* __restrict__ logits, SelectArgs a, int32_t* __restrict__ idx,
-                float* __restrict__ gates) {
+select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int C, int32_t* __restrict__ idx,
+              float* __restrict__ gates) {
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double* sc = smem + (size_t)warp * (a.E + a.groups);
   const int t = blockIdx.x * kWarps + warp;
   if (t >= a.T) return;
   const T* row = logits + (size_t)t * a.ld;
-  const int e = select_row64(row, a, sc, lane);
   float mx = -INFINITY, den = 0.0f;
-  if (a.score == SMOE_SCORE_SOFTMAX && !a.renorm) {
+  int e = -2;
+  if (lpg > 0) e = select_row32<T, NV>(row, a, lpg, C, lane, &mx, &den);
+  if (e == -2) e = select_row64(row, a, smem + (size_t)warp * (a.E + a.groups), lane);
+  if (lpg == 0 && a.score == SMOE_SCORE_SOFTMAX && !a.renorm) {
     for (int i = lane; i < a.E; i += 32) {
       const float l = to_f(row[i]);
       if (usable(l)) mx = fmaxf(mx, finite_top(l));
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+    mx = warp_max(mx);
     for (int i = lane; i < a.E; i += 32) {
       const float l = to_f(row[i]);
       if (usable(l)) den += expf(finite_top(l) - mx);
@@ -249,30 +429,173 @@ select_bwd_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t* __r
   }
 }
 
+// The same with LPR lanes for a row, which hold it in registers: 16-byte pieces p * LPR +
+// sub (p < NP) of V values.  Every value is written once; a row's selected experts are
+// passed round among its lanes.
+template <typename T, int LPR, int NP>
+__global__ void __launch_bounds__(kWarps * 32)
+select_bwd_wide_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t* __restrict__ idx,
+                       const float* __restrict__ gates, const float* __restrict__ dgates,
+                       T* __restrict__ dl, unsigned* err) {
+  constexpr int V = 16 / sizeof(T), NK = SMOE_MAX_TOPK / LPR > 1 ? SMOE_MAX_TOPK / LPR : 1;
+  const int lane = threadIdx.x & 31, sub = lane & (LPR - 1);
+  const int t = (int)(((long long)blockIdx.x * kWarps * 32 + threadIdx.x) / LPR);
+  const bool live = t < a.T;
+  const T* row = logits + (size_t)(live ? t : 0) * a.ld;
+  const bool dense = a.score == SMOE_SCORE_SOFTMAX && !a.renorm;
+  float x[NP][V];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int at = (p * LPR + sub) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[p][i] = -INFINITY;
+    if (dense && live && at < a.E) {
+      T w[V];
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(row + at);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[p][i] = usable(to_f(w[i])) ? finite_top(to_f(w[i])) : -INFINITY;
+    }
+  }
+  // this lane's selected experts: slots sub, sub + LPR
+  int e[NK];
+  float g[NK], d[NK], lsel[NK], A = 0.0f;
+#pragma unroll
+  for (int q = 0; q < NK; ++q) {
+    const int j = q * LPR + sub;
+    e[q] = -1;
+    g[q] = d[q] = lsel[q] = 0.0f;
+    if (live && j < a.k) {
+      e[q] = idx[(size_t)t * a.k + j];
+      g[q] = gates[(size_t)t * a.k + j];
+      if (e[q] < 0 || e[q] >= a.E) {
+        report_error(err, ERRBIT_DATA);
+        e[q] = -1;
+      }
+      if (e[q] >= 0 && g[q] != 0.0f) {
+        d[q] = g[q] * dgates[(size_t)t * a.k + j];
+        if (a.score == SMOE_SCORE_SIGMOID) lsel[q] = to_f(row[e[q]]);
+      }
+    }
+    A += d[q];
+  }
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) A += __shfl_xor_sync(kFull, A, off);
+  if (dense) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < V; ++i) mx = fmaxf(mx, x[p][i]);
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+    float den = 0.0f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        x[p][i] = x[p][i] > -INFINITY ? expf(x[p][i] - mx) : 0.0f;
+        den += x[p][i];
+      }
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) den += __shfl_xor_sync(kFull, den, off);
+    const float f = den > 0.0f ? -A / den : 0.0f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[p][i] *= f;
+  } else {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[p][i] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < NK; ++q) {
+      if (a.renorm) d[q] -= g[q] * (A / a.scale);
+      if (a.score == SMOE_SCORE_SIGMOID) d[q] *= 1.0f / (1.0f + expf(lsel[q]));
+      if (g[q] == 0.0f) d[q] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NK; ++q)
+    for (int j = 0; j < LPR && q * LPR + j < a.k; ++j) {
+      const int ej = __shfl_sync(kFull, e[q], j, LPR);
+      const float dj = __shfl_sync(kFull, d[q], j, LPR);
+      const int at = ej / V;  // -1 / V = 0, but then dj = 0
+      if ((at & (LPR - 1)) == sub) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if ((p * LPR + sub) * V + i == ej) x[p][i] += dj;
+      }
+    }
+  if (!live) return;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int at = (p * LPR + sub) * V;
+    if (at >= a.E) continue;
+    T w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = from_f<T>(x[p][i]);
+    *reinterpret_cast<uint4*>(dl + (size_t)t * a.E + at) = *reinterpret_cast<const uint4*>(w);
+  }
+}
+
+template <typename T>
+cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* gates, cudaStream_t s) {
+  const size_t smem = (size_t)kWarps * (a.E + a.groups) * sizeof(double);
+  const int grid = cdiv(a.T, kWarps);
+  int lpg = a.groups <= 32 ? 32 : 0;
+  while (lpg * a.groups > 32) lpg >>= 1;
+  const int C = lpg ? cdiv(a.E / a.groups, lpg) : 0;
+  // 32 values are what fits a lane's registers beside their scores
+#define SELECT(NV, L) select_kernel<T, NV><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates)
+  if (lpg == 0 || C > 32) SELECT(1, 0);
+  else if (C == 1) SELECT(1, lpg);
+  else if (C == 2) SELECT(2, lpg);
+  else if (C <= 4) SELECT(4, lpg);
+  else if (C <= 8) SELECT(8, lpg);
+  else if (C <= 16) SELECT(16, lpg);
+  else SELECT(32, lpg);
+#undef SELECT
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t select_bwd(const T* logits, const SelectArgs& a, const int32_t* idx, const float* gates,
+                       const float* dgates, T* dl, unsigned* err, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int pieces = a.E / V;
+  if (a.E % V || a.ld % V || pieces > 8 * 32) {  // rows that are not whole 16-byte pieces
+    select_bwd_kernel<T><<<cdiv(a.T, kWarps), kWarps * 32, 0, s>>>(logits, a, idx, gates, dgates, dl, err);
+    return cudaGetLastError();
+  }
+#define SELECT_BWD(LPR, NP)                                                                              \
+  select_bwd_wide_kernel<T, LPR, NP><<<cdiv(a.T, kWarps * 32 / LPR), kWarps * 32, 0, s>>>(logits, a, idx, \
+                                                                                          gates, dgates, dl, err)
+  if (pieces <= 8) SELECT_BWD(8, 1);
+  else if (pieces <= 16) SELECT_BWD(16, 1);
+  else if (pieces <= 32) SELECT_BWD(32, 1);
+  else if (pieces <= 64) SELECT_BWD(32, 2);
+  else if (pieces <= 128) SELECT_BWD(32, 4);
+  else SELECT_BWD(32, 8);
+#undef SELECT_BWD
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_select(const void* logits, const SelectArgs& a, smoe_dtype dt, int32_t* idx,
                           float* gates, cudaStream_t s) {
-  const size_t smem = (size_t)kWarps * (a.E + a.groups) * sizeof(double);
-  const int grid = cdiv(a.T, kWarps);
-  if (dt == SMOE_BF16)
-    select64_kernel<bf16><<<grid, kWarps * 32, smem, s>>>((const bf16*)logits, a, idx, gates);
-  else
-    select64_kernel<float><<<grid, kWarps * 32, smem, s>>>((const float*)logits, a, idx, gates);
-  return cudaGetLastError();
+  return dt == SMOE_BF16 ? select((const bf16*)logits, a, idx, gates, s)
+                         : select((const float*)logits, a, idx, gates, s);
 }
 
 cudaError_t launch_select_bwd(const void* logits, const SelectArgs& a, smoe_dtype dt,
                               const int32_t* idx, const float* gates, const float* dgates, void* dl,
                               unsigned* err, cudaStream_t s) {
-  const int grid = cdiv(a.T, kWarps);
-  if (dt == SMOE_BF16)
-    select_bwd_kernel<bf16><<<grid, kWarps * 32, 0, s>>>((const bf16*)logits, a, idx, gates, dgates,
-                                                         (bf16*)dl, err);
-  else
-    select_bwd_kernel<float><<<grid, kWarps * 32, 0, s>>>((const float*)logits, a, idx, gates,
-                                                          dgates, (float*)dl, err);
-  return cudaGetLastError();
+  return dt == SMOE_BF16 ? select_bwd((const bf16*)logits, a, idx, gates, dgates, (bf16*)dl, err, s)
+                         : select_bwd((const float*)logits, a, idx, gates, dgates, (float*)dl, err, s);
 }
 
 }  // namespace smoe

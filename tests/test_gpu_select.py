@@ -113,6 +113,34 @@ def test_select_unavailable_experts(score, renorm, dtype):
             assert smoe.smoe_check() == 0 and int(off[-1]) == T * k
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (4, 2), (48, 5)])
+def test_select_signed_zeros_and_wide_biases(score, groups, top_groups):
+    """Zeros of both signs tie; a bias that dwarfs the scores rounds them away in 32 bits."""
+    T, E, k = 8, 96, 5
+    logits, _ = _inputs(T, E, F32, False, 12)
+    logits[0] = 0.0
+    logits[0, ::3] = -0.0
+    logits[1, 40:] = -0.0
+    logits[1, :40] = 0.0
+    _check(logits, None, k, score, True, 1.0, groups, top_groups, 2)
+    g = torch.Generator().manual_seed(13)
+    b = 1000.0 * torch.randint(-3, 4, (E,), generator=g).float()
+    _check(logits, b, k, score, True, 1.0, groups, top_groups, 2)
+    b[::4] = 3e38
+    b[5] = math.inf
+    _check(logits, b, k, score, False, 1.0, groups, top_groups, 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [24, 33, 130, 512, 1001])
+def test_select_bias_of_zeros(E, dtype):
+    """The bias a training starts with: equal logits are equal scores."""
+    logits, _ = _inputs(60, E, dtype, False, 14)
+    _check(logits, torch.zeros(E), min(8, E), "sigmoid", True, 1.0, 1, 1, 2)
+    _check(logits, torch.zeros(E), min(8, E), "softmax", False, 1.0, 1, 1, 2)
+
+
 def test_select_strided_and_given_outputs():
     T, E, k = 45, 20, 4
     wide = torch.randn(T, 64, generator=torch.Generator().manual_seed(7)).cuda()
