@@ -13,6 +13,10 @@
 // share a head; the mean is log2 of that many shuffles.  A lane keeps its row's cosines
 // and sines for all heads of the row.
 //
+// A lane asks for the pieces of kBatch heads before it uses the first, and for a row's
+// pieces before its position: outputs may be the inputs, so the compiler does not move
+// loads across stores by itself.
+//
 // Angles: far positions need more than fp32.  inv_freq / (2 pi) is held as a 64-bit
 // fixed-point fraction of a turn, so position * fraction modulo 2^64 is the angle with
 // whole turns dropped exactly; its upper 32 bits go to sincospif.
@@ -28,15 +32,14 @@ constexpr int kMaxBlocks = 4 * 148;  // of the backward, per part: fixes the ord
 template <typename T>
 struct Geo {
   static constexpr int V = 16 / sizeof(T);  // values per 16-byte piece
+  static constexpr int kBatch = 4;          // heads loaded ahead, forward
 };
 
-__device__ __forceinline__ void load_piece(const float* p, float* v) {
-  const float4 f = *reinterpret_cast<const float4*>(p);
-  v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+__device__ __forceinline__ void unpack_piece(const uint4& u, float* v, const float*) {
+  v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
 }
-__device__ __forceinline__ void load_piece(const bf16* p, float* v) {
-  unpack8(*reinterpret_cast<const uint4*>(p), v);
-}
+__device__ __forceinline__ void unpack_piece(const uint4& u, float* v, const bf16*) { unpack8(u, v); }
 __device__ __forceinline__ void store_piece(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -63,10 +66,17 @@ __device__ __forceinline__ unsigned long long turn_fraction(float inv_freq) {
   t -= floor(t);
   return (unsigned long long)(t * 18446744073709551616.0);
 }
+template <typename T>
 __device__ __forceinline__ void turn(unsigned long long f, int pos, float* c, float* s) {
   const unsigned long long a = f * (unsigned long long)(long long)pos;
   const int hi = (int)(unsigned)((a + 0x80000000ull) >> 32);  // turns * 2^32, in [-1/2, 1/2)
-  sincospif((float)hi * 4.656612873077393e-10f, s, c);        // hi 2^-31 = turns * 2
+  if (sizeof(T) == 2) {  // values of 8 bits: sin.approx is within 2^-20.5 between -pi and pi
+    const float r = (float)hi * 1.4629180792671596e-9f;  // hi 2 pi / 2^32
+    *s = __sinf(r);
+    *c = __cosf(r);
+  } else {
+    sincospif((float)hi * 4.656612873077393e-10f, s, c);  // hi 2^-31 = turns * 2
+  }
 }
 
 // Frequency index of pair i (i < V) of lane `sub`.
@@ -142,7 +152,7 @@ __device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
 template <typename T, int DH, bool kInter, bool kServe>
 __global__ void __launch_bounds__(kThreads)
 qk_fwd_kernel(const __grid_constant__ KArgs g) {
-  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH;
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH, HB = Geo<T>::kBatch;
   const QkArgs& a = g.a;
   int part = PART_Q, blk = blockIdx.x;
   while (part < PART_V && blk >= g.nb[part]) blk -= g.nb[part++];
@@ -174,6 +184,20 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
     bool live = u < units;
     const int row = live ? (int)(u / chunks) : 0;
     const int h0 = live ? (int)(u % chunks) * g.hpu : 0;
+    const T* xr = x + row * ldx;
+    uint4 raw[HB][2];
+    auto fetch = [&](int hh) {
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
+        if (live && hh + j < g.hpu && h0 + hh + j < heads) {
+          const T* p = xr + (h0 + hh + j) * DH + sub * V;
+          raw[j][0] = *reinterpret_cast<const uint4*>(p);
+          raw[j][1] = *reinterpret_cast<const uint4*>(p + DH / 2);
+        }
+      }
+    };
+    fetch(0);
     int t = row, pos = 0, off = 0;
     int64_t page = 0;
     if (live && part == PART_Q) {
@@ -191,20 +215,19 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       c[i] = 1.0f; s[i] = 0.0f;
-      if (rot) turn(fr[i], pos, &c[i], &s[i]);
+      if (rot) turn<T>(fr[i], pos, &c[i], &s[i]);
     }
-    const T* xr = x + row * ldx;
-#pragma unroll 4
-    for (int hh = 0; hh < g.hpu; ++hh) {
+    for (int h4 = 0; h4 < g.hpu; h4 += HB) {
+     if (h4 > 0) fetch(h4);
+#pragma unroll
+     for (int j = 0; j < HB; ++j) {
+      const int hh = h4 + j;
+      if (hh >= g.hpu) break;
       const int h = h0 + hh;
       const bool on = live && h < heads;
       float v[2 * V];
-#pragma unroll
-      for (int i = 0; i < 2 * V; ++i) v[i] = 0.0f;
-      if (on) {
-        load_piece(xr + h * DH + sub * V, v);
-        load_piece(xr + h * DH + DH / 2 + sub * V, v + V);
-      }
+      unpack_piece(raw[j][0], v, (const T*)nullptr);
+      unpack_piece(raw[j][1], v + V, (const T*)nullptr);
       if (norm) {
         float ss = 0.0f;
 #pragma unroll
@@ -255,14 +278,15 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
           }
         }
       }
+     }
     }
   }
 }
 
 template <typename T, int DH, bool kInter>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 qk_bwd_kernel(const __grid_constant__ KArgs g) {
-  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH;
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH, HB = Geo<T>::kBatch / 2;
   __shared__ float red[kThreads / 32][DH];
   const QkArgs& a = g.a;
   const int part = (int)blockIdx.x < g.nb[0] ? PART_Q : PART_K;
@@ -297,6 +321,26 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
     bool live = u < units;
     const int row = live ? (int)(u / chunks) : 0;
     const int h0 = live ? (int)(u % chunks) * g.hpu : 0;
+    const T* xr = x + row * ldx;
+    const T* yr = dy + row * ldy;
+    uint4 raw[HB][4];
+    auto fetch = [&](int hh) {
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[j][i] = make_uint4(0, 0, 0, 0);
+        if (live && hh + j < g.hpu && h0 + hh + j < heads) {
+          const int at = (h0 + hh + j) * DH + sub * V;
+          raw[j][0] = *reinterpret_cast<const uint4*>(yr + at);
+          raw[j][1] = *reinterpret_cast<const uint4*>(yr + at + DH / 2);
+          if (a.norm) {
+            raw[j][2] = *reinterpret_cast<const uint4*>(xr + at);
+            raw[j][3] = *reinterpret_cast<const uint4*>(xr + at + DH / 2);
+          }
+        }
+      }
+    };
+    fetch(0);
     int t = row;
     if (live && part == PART_Q) {
       int p = row;
@@ -312,25 +356,21 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       c[i] = 1.0f; s[i] = 0.0f;
-      if (rot) turn(fr[i], pos, &c[i], &s[i]);
+      if (rot) turn<T>(fr[i], pos, &c[i], &s[i]);
     }
-    const T* xr = x + row * ldx;
-    const T* yr = dy + row * ldy;
-#pragma unroll 2
-    for (int hh = 0; hh < g.hpu; ++hh) {
+    for (int h2 = 0; h2 < g.hpu; h2 += HB) {
+     if (h2 > 0) fetch(h2);
+#pragma unroll
+     for (int j = 0; j < HB; ++j) {
+      const int hh = h2 + j;
+      if (hh >= g.hpu) break;
       const int h = h0 + hh;
       const bool on = live && h < heads;
       float v[2 * V], d[2 * V];
-#pragma unroll
-      for (int i = 0; i < 2 * V; ++i) v[i] = d[i] = 0.0f;
-      if (on) {
-        load_piece(yr + h * DH + sub * V, d);
-        load_piece(yr + h * DH + DH / 2 + sub * V, d + V);
-        if (a.norm) {
-          load_piece(xr + h * DH + sub * V, v);
-          load_piece(xr + h * DH + DH / 2 + sub * V, v + V);
-        }
-      }
+      unpack_piece(raw[j][0], d, (const T*)nullptr);
+      unpack_piece(raw[j][1], d + V, (const T*)nullptr);
+      unpack_piece(raw[j][2], v, (const T*)nullptr);
+      unpack_piece(raw[j][3], v + V, (const T*)nullptr);
       if (rot) rotate<V, kInter>(d, c, s, -1.0f);
       if (a.norm) {
         float ss = 0.0f, dot = 0.0f;
@@ -355,6 +395,7 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
         store_piece(out + sub * V, d);
         store_piece(out + DH / 2 + sub * V, d + V);
       }
+     }
     }
   }
   if (!want_dw) return;
@@ -386,6 +427,7 @@ qk_dw_sum_kernel(const float* __restrict__ partial, int nq, int nk, int DH, floa
   const int b0 = part == 0 ? 0 : nq, nb = part == 0 ? nq : nk;
   if (!out) return;
   float v = 0.0f;
+#pragma unroll 8
   for (int b = threadIdx.y; b < nb; b += 32) v += partial[(size_t)(b0 + b) * DH + col];
   red[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
