@@ -9,9 +9,9 @@ raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -111,7 +111,7 @@ def lib():
     L.smoe_moa_attn_workspace_size.argtypes = [_c_int] * 4
     L.smoe_moa_attn_fwd.argtypes = [_vp, _vp, _vp, _vp] + [_c_int] * 6 + [_vp, _vp, _vp, _c_size, _vp]
     L.smoe_moa_attn_bwd.argtypes = [_vp] * 7 + [_c_int] * 6 + [_vp] * 4 + [_c_size, _vp]
-    i64, desc, cache = ctypes.c_int64, ctypes.POINTER(QkDesc), ctypes.POINTER(KvCache)
+    i64, desc, cache = ctypes.c_int64, _vp, _vp  # a Structure by reference, or its bytes
     L.smoe_route_select.argtypes = [_vp, _c_int, _vp] + [_c_int] * 5 + [ctypes.c_float] + \
         [_c_int] * 4 + [_vp] * 3
     L.smoe_route_select_bwd.argtypes = [_vp, _c_int] + [_vp] * 3 + [_c_int] * 5 + \
@@ -357,39 +357,63 @@ def smoe_moa_attn_bwd(q, k, v, o, lse, dout, sorted_slot, kslots, L, heads, stre
     return dq, dk, dv
 
 
+# ---- calls whose host side counts: decode steps of a few microseconds each -----------
+# Their checks are one expression a tensor, which also gives the address; only where it
+# fails is the reason looked for.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_QK = struct.Struct("8if")      # smoe_qk_desc
+_KV = struct.Struct("6P7q6i")   # smoe_kv_cache
+
+
+def _elsewhere(dev, stream):
+    """Whether a call has to change the current device or stream."""
+    return stream is not None or dev != torch.cuda.current_device()
+
+
 def _scope(t, stream):
     """Context in which a call on ``t`` runs: ``stream``, whose allocations then belong to
     it, or the current stream of ``t``'s device."""
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
+    if stream is None:
         return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
-def _same_device(ref, *named):
-    for t, name in named:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+def _refuse(t, name, dtype, shape, dev):
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
-def _rows(t, name, dtype, shape):
-    """Check a matrix whose rows may lie apart (unit stride inside a row); its row stride."""
+def _at(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape on device ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+
+
+def _at_opt(t, name, dtype, shape, dev):
+    return None if t is None else _at(t, name, dtype, shape, dev)
+
+
+def _rows(t, name, dtype, shape, dev):
+    """(address, row stride) of a matrix whose rows may lie apart (unit stride inside)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        ld, one = t.stride()
+        if one == 1 or shape[1] <= 1:
+            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+        raise ValueError(f"{name} must have unit stride inside its rows")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit stride inside its rows")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    _refuse(t.contiguous(), name, dtype, shape, dev)
 
 
-def _dp(t):
-    return None if t is None else t.data_ptr()
+def _matrix(t, name):
+    """(shape, device index) of a CUDA matrix."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise TypeError(f"{name} must be a CUDA tensor of two dimensions")
+    return t.shape, t.get_device()
 
 
 def _score(name):
@@ -402,90 +426,65 @@ def smoe_route_select(logits, k, bias=None, *, score="softmax", renorm=True, sca
                       top_groups=1, group_top=2, topk_idx=None, gates=None, stream=None):
     """Top-k routing from logits [T, E] (fp32 or bf16; the rows may lie apart): scores,
     selection bias, groups, gates (see smoe.h).  Returns (topk_idx [T, k], gates [T, k])."""
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise TypeError("logits must be a [T, E] CUDA tensor")
-    T, E = logits.shape
-    ld = _rows(logits, "logits", logits.dtype, logits.shape)
+    (T, E), dev = _matrix(logits, "logits")
+    if _elsewhere(dev, stream):
+        with _scope(logits, stream):
+            return smoe_route_select(logits, k, bias, score=score, renorm=renorm, scale=scale,
+                                     groups=groups, top_groups=top_groups, group_top=group_top,
+                                     topk_idx=topk_idx, gates=gates)
     dt = _dt(logits)
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (E,))
-    _same_device(logits, (bias, "bias"), (topk_idx, "topk_idx"), (gates, "gates"))
-    with _scope(logits, stream):
-        if topk_idx is None:
-            topk_idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-        else:
-            _need(topk_idx, "topk_idx", torch.int32, (T, k))
-        if gates is None:
-            gates = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-        else:
-            _need(gates, "gates", torch.float32, (T, k))
-        _check(lib().smoe_route_select(_dp(logits), ld, _dp(bias), T, E, k, _score(score),
-                                       int(renorm), scale, groups, top_groups, group_top, dt,
-                                       _dp(topk_idx), _dp(gates), _stream()))
+    x, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
+    b = _at_opt(bias, "bias", torch.float32, (E,), dev)
+    if topk_idx is None:
+        topk_idx = logits.new_empty((T, k), dtype=torch.int32)
+    if gates is None:
+        gates = logits.new_empty((T, k), dtype=torch.float32)
+    _check(lib().smoe_route_select(x, ld, b, T, E, k, _score(score), 1 if renorm else 0, scale, groups,
+                                   top_groups, group_top, dt,
+                                   _at(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+                                   _at(gates, "gates", torch.float32, (T, k), dev), _raw_stream(dev)))
     return topk_idx, gates
 
 
 def smoe_route_select_bwd(logits, topk_idx, gates, dgates, *, score="softmax", renorm=True,
                           scale=1.0, dlogits=None, stream=None):
     """Gradient [T, E] of the logits of smoe_route_select, in their dtype."""
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise TypeError("logits must be a [T, E] CUDA tensor")
-    T, E = logits.shape
-    ld = _rows(logits, "logits", logits.dtype, logits.shape)
+    (T, E), dev = _matrix(logits, "logits")
+    if _elsewhere(dev, stream):
+        with _scope(logits, stream):
+            return smoe_route_select_bwd(logits, topk_idx, gates, dgates, score=score, renorm=renorm,
+                                         scale=scale, dlogits=dlogits)
     dt = _dt(logits)
-    _need(topk_idx, "topk_idx", torch.int32)
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
-        raise ValueError(f"topk_idx must have shape ({T}, k), got {tuple(topk_idx.shape)}")
-    k = topk_idx.shape[1]
-    _need(gates, "gates", torch.float32, (T, k))
-    _need(dgates, "dgates", torch.float32, (T, k))
-    _same_device(logits, (topk_idx, "topk_idx"), (gates, "gates"), (dgates, "dgates"),
-                 (dlogits, "dlogits"))
-    with _scope(logits, stream):
-        if dlogits is None:
-            dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        else:
-            _need(dlogits, "dlogits", logits.dtype, (T, E))
-        _check(lib().smoe_route_select_bwd(_dp(logits), ld, _dp(topk_idx), _dp(gates), _dp(dgates),
-                                           T, E, k, _score(score), int(renorm), scale, dt,
-                                           _dp(dlogits), _stream()))
+    x, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
+    (_, k), _ = _matrix(topk_idx, "topk_idx")
+    i = _at(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+    g = _at(gates, "gates", torch.float32, (T, k), dev)
+    dg = _at(dgates, "dgates", torch.float32, (T, k), dev)
+    if dlogits is None:
+        dlogits = logits.new_empty((T, E))
+    _check(lib().smoe_route_select_bwd(x, ld, i, g, dg, T, E, k, _score(score), 1 if renorm else 0, scale,
+                                       dt, _at(dlogits, "dlogits", logits.dtype, (T, E), dev),
+                                       _raw_stream(dev)))
     return dlogits
 
 
-def _qk_shapes(q, k, sorted_slot, kslots, q_heads, kv_heads):
-    """(T, head_dim, dtype, device reference) of a call on q rows, k rows or both."""
-    ref = q if q is not None else k
-    if ref is None:
-        raise ValueError("q and k are both None")
-    for t, n in ((q, "q"), (k, "k")):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 2):
-            raise TypeError(f"{n} must be a matrix of rows")
+def _qk_sizes(q, k, kslots, q_heads, kv_heads):
+    """(T, head_dim, one of the tensors, its device) of a call on q rows, k rows or both."""
     if kslots < 1 or q_heads < 1 or kv_heads < 1:
         raise ValueError("kslots, q_heads and kv_heads must be at least 1")
     if k is not None:
-        T, heads = k.shape[0], kv_heads
+        (T, width), dev = _matrix(k, "k")
+        ref, heads = k, kv_heads
+    elif q is not None:
+        (rows, width), dev = _matrix(q, "q")
+        if rows % kslots:
+            raise ValueError(f"q has {rows} rows, not a multiple of kslots = {kslots}")
+        T, ref, heads = rows // kslots, q, q_heads
     else:
-        if q.shape[0] % kslots:
-            raise ValueError(f"q has {q.shape[0]} rows, not a multiple of kslots = {kslots}")
-        T, heads = q.shape[0] // kslots, q_heads
-    width = ref.shape[1] if k is None else k.shape[1]
+        raise ValueError("q and k are both None")
     if width % heads:
         raise ValueError(f"rows of {width} values do not divide into {heads} heads")
-    if sorted_slot is not None:
-        _need(sorted_slot, "sorted_slot", torch.int32, (T * kslots,))
-    return T, width // heads, ref
-
-
-def _qk_params(dh, T, positions, inv_freq, wq, wk, need_positions):
-    if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32, (dh // 2,))
-        if need_positions and positions is None:
-            raise ValueError("rotation needs positions")
-    if positions is not None:
-        _need(positions, "positions", torch.int32, (T,))
-    for w, n in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _need(w, n, torch.float32, (dh,))
+    return T, width // heads, ref, dev
 
 
 def smoe_moa_qk_norm_rope_fwd(q, k, sorted_slot, kslots, *, q_heads, kv_heads, positions=None,
@@ -494,29 +493,36 @@ def smoe_moa_qk_norm_rope_fwd(q, k, sorted_slot, kslots, *, q_heads, kv_heads, p
     """Per-head RMS norm and position rotation of grouped queries q [T*kslots,
     q_heads*head_dim] and keys k [T, kv_heads*head_dim] (either may be None); see smoe.h.
     Rows may lie apart.  Returns (q_out, k_out)."""
-    T, dh, ref = _qk_shapes(q, k, sorted_slot, kslots, q_heads, kv_heads)
-    _qk_params(dh, T, positions, inv_freq, wq, wk, True)
-    _same_device(ref, (q, "q"), (k, "k"), (sorted_slot, "sorted_slot"), (positions, "positions"),
-                 (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"), (q_out, "q_out"), (k_out, "k_out"))
-    desc = QkDesc(T, kslots, q_heads, kv_heads, dh, _dt(ref), int(norm), int(interleaved), eps)
+    T, dh, ref, dev = _qk_sizes(q, k, kslots, q_heads, kv_heads)
+    if _elsewhere(dev, stream):
+        with _scope(ref, stream):
+            return smoe_moa_qk_norm_rope_fwd(q, k, sorted_slot, kslots, q_heads=q_heads, kv_heads=kv_heads,
+                                             positions=positions, inv_freq=inv_freq, wq=wq, wk=wk, eps=eps,
+                                             norm=norm, interleaved=interleaved, q_out=q_out, k_out=k_out)
+    dt, code, f32, i32 = ref.dtype, _dt(ref), torch.float32, torch.int32
+    desc = _QK.pack(T, kslots, q_heads, kv_heads, dh, code, 1 if norm else 0, 1 if interleaved else 0, eps)
+    x = y = xo = yo = None
     ldq = ldk = 0
     if q is not None:
-        ldq = _rows(q, "q", ref.dtype, (T * kslots, q_heads * dh))
+        shape = (T * kslots, q_heads * dh)
+        x, ldq = _rows(q, "q", dt, shape, dev)
+        if q_out is None:
+            q_out = q.new_empty(shape)
+        xo = _at(q_out, "q_out", dt, shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without its input")
     if k is not None:
-        ldk = _rows(k, "k", ref.dtype, (T, kv_heads * dh))
-    with _scope(ref, stream):
-        for t, out, n in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-            if out is not None:
-                if t is None:
-                    raise ValueError(f"{n} without its input")
-                _need(out, n, t.dtype, t.shape)
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _check(lib().smoe_moa_qk_norm_rope_fwd(
-            ctypes.byref(desc), _dp(q), ldq, _dp(k), ldk, _dp(sorted_slot), _dp(positions),
-            _dp(inv_freq), _dp(wq), _dp(wk), _dp(q_out), _dp(k_out), _stream()))
+        shape = (T, kv_heads * dh)
+        y, ldk = _rows(k, "k", dt, shape, dev)
+        if k_out is None:
+            k_out = k.new_empty(shape)
+        yo = _at(k_out, "k_out", dt, shape, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without its input")
+    _check(lib().smoe_moa_qk_norm_rope_fwd(
+        desc, x, ldq, y, ldk, _at_opt(sorted_slot, "sorted_slot", i32, (T * kslots,), dev),
+        _at_opt(positions, "positions", i32, (T,), dev), _at_opt(inv_freq, "inv_freq", f32, (dh // 2,), dev),
+        _at_opt(wq, "wq", f32, (dh,), dev), _at_opt(wk, "wk", f32, (dh,), dev), xo, yo, _raw_stream(dev)))
     return q_out, k_out
 
 
@@ -525,73 +531,85 @@ def smoe_moa_qk_norm_rope_bwd(dq_out, dk_out, q, k, sorted_slot, kslots, *, q_he
                               interleaved=False, stream=None):
     """Gradients of smoe_moa_qk_norm_rope_fwd: (dq, dk, dwq, dwk); dwq and dwk (fp32) are
     None without their weights, dq and dk without dq_out and dk_out."""
-    T, dh, ref = _qk_shapes(dq_out, dk_out, sorted_slot, kslots, q_heads, kv_heads)
-    _qk_params(dh, T, positions, inv_freq, wq, wk, True)
-    _same_device(ref, (dq_out, "dq_out"), (dk_out, "dk_out"), (q, "q"), (k, "k"),
-                 (sorted_slot, "sorted_slot"), (positions, "positions"), (inv_freq, "inv_freq"),
-                 (wq, "wq"), (wk, "wk"))
-    desc = QkDesc(T, kslots, q_heads, kv_heads, dh, _dt(ref), int(norm), int(interleaved), eps)
-    ld = [0, 0, 0, 0]
-    sq, sk = (T * kslots, q_heads * dh), (T, kv_heads * dh)
-    for i, (t, n, s, dy) in enumerate(((dq_out, "dq_out", sq, dq_out), (dk_out, "dk_out", sk, dk_out),
-                                       (q, "q", sq, dq_out), (k, "k", sk, dk_out))):
-        if dy is not None and (i < 2 or norm):
-            ld[i] = _rows(t, n, ref.dtype, s)
-    with _scope(ref, stream):
-        dev = ref.device
-        dq = dk = dwq = dwk = ws = None
-        if dq_out is not None:
-            dq = torch.empty(sq, dtype=ref.dtype, device=dev)
-            dwq = torch.empty((dh,), dtype=torch.float32, device=dev) if wq is not None else None
-        if dk_out is not None:
-            dk = torch.empty(sk, dtype=ref.dtype, device=dev)
-            dwk = torch.empty((dh,), dtype=torch.float32, device=dev) if wk is not None else None
-        nbytes = 0
-        if dwq is not None or dwk is not None:
-            nbytes = lib().smoe_moa_qk_norm_rope_bwd_workspace_size(ctypes.byref(desc))
-            ws = _workspace(nbytes, dev)
-        _check(lib().smoe_moa_qk_norm_rope_bwd(
-            ctypes.byref(desc), _dp(dq_out), ld[0], _dp(dk_out), ld[1], _dp(q), ld[2], _dp(k), ld[3],
-            _dp(sorted_slot), _dp(positions), _dp(inv_freq), _dp(wq), _dp(wk), _dp(dq), _dp(dk),
-            _dp(dwq), _dp(dwk), _dp(ws), nbytes, _stream()))
+    T, dh, ref, dev = _qk_sizes(dq_out, dk_out, kslots, q_heads, kv_heads)
+    if _elsewhere(dev, stream):
+        with _scope(ref, stream):
+            return smoe_moa_qk_norm_rope_bwd(dq_out, dk_out, q, k, sorted_slot, kslots, q_heads=q_heads,
+                                             kv_heads=kv_heads, positions=positions, inv_freq=inv_freq,
+                                             wq=wq, wk=wk, eps=eps, norm=norm, interleaved=interleaved)
+    dt, code, f32, i32 = ref.dtype, _dt(ref), torch.float32, torch.int32
+    desc = _QK.pack(T, kslots, q_heads, kv_heads, dh, code, 1 if norm else 0, 1 if interleaved else 0, eps)
+    w1, w2 = _at_opt(wq, "wq", f32, (dh,), dev), _at_opt(wk, "wk", f32, (dh,), dev)
+    dq = dk = dwq = dwk = None
+    dx = dy = x = y = ox = oy = ow = ov = ws = None
+    lddx = lddy = ldx = ldy = nbytes = 0
+    if dq_out is not None:
+        shape = (T * kslots, q_heads * dh)
+        dx, lddx = _rows(dq_out, "dq_out", dt, shape, dev)
+        if norm:
+            x, ldx = _rows(q, "q", dt, shape, dev)
+        dq = dq_out.new_empty(shape)
+        ox = dq.data_ptr()
+        if w1 is not None:
+            dwq = wq.new_empty((dh,))
+            ow = dwq.data_ptr()
+    if dk_out is not None:
+        shape = (T, kv_heads * dh)
+        dy, lddy = _rows(dk_out, "dk_out", dt, shape, dev)
+        if norm:
+            y, ldy = _rows(k, "k", dt, shape, dev)
+        dk = dk_out.new_empty(shape)
+        oy = dk.data_ptr()
+        if w2 is not None:
+            dwk = wk.new_empty((dh,))
+            ov = dwk.data_ptr()
+    if ow is not None or ov is not None:
+        nbytes = lib().smoe_moa_qk_norm_rope_bwd_workspace_size(desc)
+        buf = ref.new_empty(nbytes, dtype=torch.uint8)
+        ws = buf.data_ptr()
+    _check(lib().smoe_moa_qk_norm_rope_bwd(
+        desc, dx, lddx, dy, lddy, x, ldx, y, ldy,
+        _at_opt(sorted_slot, "sorted_slot", i32, (T * kslots,), dev),
+        _at_opt(positions, "positions", i32, (T,), dev), _at_opt(inv_freq, "inv_freq", f32, (dh // 2,), dev),
+        w1, w2, ox, oy, ow, ov, ws, nbytes, _raw_stream(dev)))
     return dq, dk, dwq, dwk
 
 
+def _page_strides(t, name, dtype, shape, dev):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        page, token, head, one = t.stride()
+        if one != 1 and shape[3] > 1:
+            raise ValueError(f"{name} must have unit stride inside a head")
+        return t.data_ptr(), page, token, head
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    _refuse(t.contiguous(), name, dtype, shape, dev)
+
+
 def _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, written):
-    """The C description of a paged cache from its tensors, checked."""
+    """(smoe_kv_cache, B, kv_heads, head_dim) of a paged cache, checked."""
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda or k_cache.dim() != 4:
+        raise TypeError("k_cache must be a [num_pages, page_size, kv_heads, head_dim] CUDA tensor")
+    dev, shape = k_cache.get_device(), k_cache.shape
+    pages, page, heads, dh = shape
     dt = torch.bfloat16 if k_scale is None else torch.uint8
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
-            raise TypeError(f"{n} must be a [num_pages, page_size, kv_heads, head_dim] CUDA tensor")
-        if t.dtype != dt:
-            raise TypeError(f"{n} must be {dt}, got {t.dtype}")
-        if t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError(f"{n} must have unit stride inside a head")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    pages, page, heads, dh = k_cache.shape
-    sk, sv = k_cache.stride(), v_cache.stride()
-    if written:
-        for st, n in ((sk, "k_cache"), (sv, "v_cache")):
-            if any(st[i] == 0 and k_cache.shape[i] > 1 for i in range(3)):
-                raise ValueError(f"{n} is written and must not be an expanded tensor")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go together")
+    k, kp, kt, kh = _page_strides(k_cache, "k_cache", dt, shape, dev)
+    v, vp, vt, vh = _page_strides(v_cache, "v_cache", dt, shape, dev)
+    if written and not (kp and kt and kh and vp and vt and vh):
+        for name, st in (("k_cache", (kp, kt, kh)), ("v_cache", (vp, vt, vh))):
+            if any(st[i] == 0 and shape[i] > 1 for i in range(3)):
+                raise ValueError(f"{name} is written and must not be an expanded tensor")
+    ks = vs = 0
     if k_scale is not None:
-        _need(k_scale, "k_scale", torch.float32, (pages, page, heads))
-        _need(v_scale, "v_scale", torch.float32, (pages, page, heads))
-    _need(seq_lens, "seq_lens", torch.int32)
-    B = seq_lens.numel()
-    if seq_lens.dim() != 1:
-        raise ValueError("seq_lens must have shape (B,)")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise TypeError("block_table must be a [B, max_pages] CUDA tensor")
-    ldt = _rows(block_table, "block_table", torch.int32, (B, block_table.shape[1]))
-    _same_device(k_cache, (v_cache, "v_cache"), (block_table, "block_table"),
-                 (seq_lens, "seq_lens"), (k_scale, "k_scale"), (v_scale, "v_scale"))
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), _dp(k_scale), _dp(v_scale),
-                   block_table.data_ptr(), seq_lens.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
-                   sv[2], ldt, pages, page, block_table.shape[1], B, heads, dh)
+        ks = _at(k_scale, "k_scale", torch.float32, shape[:3], dev)
+        vs = _at(v_scale, "v_scale", torch.float32, shape[:3], dev)
+    elif v_scale is not None:
+        raise ValueError("k_scale and v_scale go together")
+    (B, max_pages), _ = _matrix(block_table, "block_table")
+    table, ldt = _rows(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    lens = _at(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    return _KV.pack(k, v, ks, vs, table, lens, kp, kt, kh, vp, vt, vh, ldt, pages, page, max_pages, B,
+                    heads, dh), B, heads, dh
 
 
 def smoe_moa_cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, sorted_slot, kslots,
@@ -602,33 +620,34 @@ def smoe_moa_cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, sort
     store keys and values in the paged cache (bf16, or uint8 e4m3 codes with k_scale and
     v_scale), at the places that seq_lens, block_table and starts give them (see smoe.h).
     Rows of q_out that stand for no token are not written."""
-    c = _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, True)
-    if not isinstance(k, torch.Tensor) or k.dim() != 2:
-        raise TypeError("k must be a matrix of rows")
-    T, dh = k.shape[0], c.head_dim
-    if starts is not None:
-        _need(starts, "starts", torch.int32, (c.B + 1,))
-    if sorted_slot is not None:
-        _need(sorted_slot, "sorted_slot", torch.int32, (T * kslots,))
-    _qk_params(dh, T, None, inv_freq, wq, wk, False)
-    _same_device(k_cache, (q, "q"), (k, "k"), (v, "v"), (sorted_slot, "sorted_slot"),
-                 (starts, "starts"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"),
-                 (q_out, "q_out"))
-    bf = torch.bfloat16
-    ldk = _rows(k, "k", bf, (T, c.kv_heads * dh))
-    ldv = _rows(v, "v", bf, (T, c.kv_heads * dh))
-    ldq = 0 if q is None else _rows(q, "q", bf, (T * kslots, q_heads * dh))
-    desc = QkDesc(T, kslots, q_heads, c.kv_heads, dh, BF16, int(norm), int(interleaved), eps)
-    with _scope(k_cache, stream):
-        if q_out is not None:
-            if q is None:
-                raise ValueError("q_out without q")
-            _need(q_out, "q_out", bf, q.shape)
-        elif q is not None:
-            q_out = torch.empty(q.shape, dtype=bf, device=q.device)
-        _check(lib().smoe_moa_cache_append(
-            ctypes.byref(desc), _dp(q), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, _dp(sorted_slot),
-            _dp(starts), _dp(inv_freq), _dp(wq), _dp(wk), ctypes.byref(c), _dp(q_out), _stream()))
+    cache, B, heads, dh = _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, True)
+    dev = k_cache.get_device()
+    if _elsewhere(dev, stream):
+        with _scope(k_cache, stream):
+            return smoe_moa_cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, sorted_slot,
+                                         kslots, q_heads, starts=starts, inv_freq=inv_freq, wq=wq, wk=wk,
+                                         eps=eps, norm=norm, interleaved=interleaved, k_scale=k_scale,
+                                         v_scale=v_scale, q_out=q_out)
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    (T, _), _ = _matrix(k, "k")
+    y, ldk = _rows(k, "k", bf, (T, heads * dh), dev)
+    z, ldv = _rows(v, "v", bf, (T, heads * dh), dev)
+    x = xo = None
+    ldq = 0
+    if q is not None:
+        shape = (T * kslots, q_heads * dh)
+        x, ldq = _rows(q, "q", bf, shape, dev)
+        if q_out is None:
+            q_out = q.new_empty(shape)
+        xo = _at(q_out, "q_out", bf, shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(lib().smoe_moa_cache_append(
+        _QK.pack(T, kslots, q_heads, heads, dh, BF16, 1 if norm else 0, 1 if interleaved else 0, eps), x, ldq,
+        y, ldk, z, ldv, _at_opt(sorted_slot, "sorted_slot", i32, (T * kslots,), dev),
+        _at_opt(starts, "starts", i32, (B + 1,), dev), _at_opt(inv_freq, "inv_freq", f32, (dh // 2,), dev),
+        _at_opt(wq, "wq", f32, (dh,), dev), _at_opt(wk, "wk", f32, (dh,), dev), cache, xo,
+        _raw_stream(dev)))
     return q_out
 
 
@@ -637,26 +656,25 @@ def smoe_moa_decode(q, k_cache, v_cache, block_table, seq_lens, sorted_slot, ksl
     """Attention of the newest token of each sequence over the paged cache (see smoe.h):
     q [B*kslots, q_heads*head_dim] bf16, grouped rows (sorted_slot None: row = slot).
     Returns (o like q, lse [B*kslots, q_heads] fp32)."""
-    c = _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, False)
-    rows, width = c.B * kslots, q_heads * c.head_dim
-    ldq = _rows(q, "q", torch.bfloat16, (rows, width))
-    if sorted_slot is not None:
-        _need(sorted_slot, "sorted_slot", torch.int32, (rows,))
-    _same_device(k_cache, (q, "q"), (sorted_slot, "sorted_slot"), (o, "o"), (lse, "lse"))
-    with _scope(k_cache, stream):
-        if o is None:
-            o = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device)
-        else:
-            _need(o, "o", torch.bfloat16, (rows, width))
-        if lse is None:
-            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device)
-        else:
-            _need(lse, "lse", torch.float32, (rows, q_heads))
-        nbytes = lib().smoe_moa_decode_workspace_size(c.B, kslots, q_heads, c.kv_heads, c.head_dim)
-        ws = _workspace(nbytes, q.device)
-        _check(lib().smoe_moa_decode(q.data_ptr(), ldq, _dp(sorted_slot), kslots, q_heads,
-                                     ctypes.byref(c), o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                     nbytes, _stream()))
+    cache, B, heads, dh = _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, False)
+    dev = k_cache.get_device()
+    if _elsewhere(dev, stream):
+        with _scope(k_cache, stream):
+            return smoe_moa_decode(q, k_cache, v_cache, block_table, seq_lens, sorted_slot, kslots, q_heads,
+                                   k_scale=k_scale, v_scale=v_scale, o=o, lse=lse)
+    rows, shape = B * kslots, (B * kslots, q_heads * dh)
+    x, ldq = _rows(q, "q", torch.bfloat16, shape, dev)
+    slots = _at_opt(sorted_slot, "sorted_slot", torch.int32, (rows,), dev)
+    if o is None:
+        o = q.new_empty(shape)
+    if lse is None:
+        lse = q.new_empty((rows, q_heads), dtype=torch.float32)
+    nbytes = lib().smoe_moa_decode_workspace_size(B, kslots, q_heads, heads, dh)
+    ws = q.new_empty(nbytes or 1, dtype=torch.uint8)
+    _check(lib().smoe_moa_decode(x, ldq, slots, kslots, q_heads, cache,
+                                 _at(o, "o", torch.bfloat16, shape, dev),
+                                 _at(lse, "lse", torch.float32, (rows, q_heads), dev), ws.data_ptr(), nbytes,
+                                 _raw_stream(dev)))
     return o, lse
 
 
