@@ -379,7 +379,7 @@ int smoe_moa_qk_norm_rope_bwd(const smoe_qk_desc* desc, const void* dyq, int64_t
  * (elements; head_dim of them in a row; any order of page, token and head).  bf16,
  * or with k_scale and v_scale (both, [num_pages, page_size, kv_heads] fp32) e4m3
  * codes of one byte, a value being code * scale: scale = amax / 448 of the head's
- * row (1 for an all-zero row), as smoe_quantize_weights_fp8's.
+ * row (1 for an all-zero row, else at least 2^-126), as smoe_quantize_weights_fp8's.
  * seq_lens[b]: tokens of sequence b, the new ones included; 0 marks an unused row of
  * the batch.  Entries of block_table beyond a sequence's pages are not read.
  *

@@ -27,7 +27,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 4 * 148;  // of the backward, per part: fixes the order of dw's sums
+constexpr int kBlocks = 2 * 148;  // two on each of 148 SMs; the backward's fixes the order of dw's sums
 
 template <typename T>
 struct Geo {
@@ -150,7 +150,7 @@ __device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
 }
 
 template <typename T, int DH, bool kInter, bool kServe>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 qk_fwd_kernel(const __grid_constant__ KArgs g) {
   constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH, HB = Geo<T>::kBatch;
   const QkArgs& a = g.a;
@@ -232,7 +232,7 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) ss += v[i] * v[i];
-        const float r = 1.0f / sqrtf(head_sum<LPH>(ss) * (1.0f / DH) + a.eps);
+        const float r = rsqrtf(head_sum<LPH>(ss) * (1.0f / DH) + a.eps);
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) v[i] *= r * w[i];
       }
@@ -259,7 +259,8 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
 #pragma unroll
           for (int i = 0; i < 2 * V; ++i) m = fmaxf(m, fabsf(v[i]));
           m = head_max<LPH>(m);
-          const float sc = m > 0.0f ? m / 448.0f : 1.0f;
+          // (at least the smallest normal number, whose reciprocal is finite)
+          const float sc = m > 0.0f ? fmaxf(m / 448.0f, 1.17549435e-38f) : 1.0f, inv = 1.0f / sc;
           if (on) {
             uint8_t* out = (uint8_t*)(is_k ? g.c.k : g.c.v) + at;
 #pragma unroll
@@ -267,7 +268,7 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
               uint16_t q[V / 2];
 #pragma unroll
               for (int i = 0; i < V / 2; ++i)
-                q[i] = e4m3_pair(v[half * V + 2 * i] / sc, v[half * V + 2 * i + 1] / sc);
+                q[i] = e4m3_pair(v[half * V + 2 * i] * inv, v[half * V + 2 * i + 1] * inv);
               uint2 u8;
               u8.x = q[0] | ((uint32_t)q[1] << 16);
               u8.y = q[V / 2 - 2] | ((uint32_t)q[V / 2 - 1] << 16);
@@ -373,21 +374,22 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
       unpack_piece(raw[j][3], v + V, (const T*)nullptr);
       if (rot) rotate<V, kInter>(d, c, s, -1.0f);
       if (a.norm) {
-        float ss = 0.0f, dot = 0.0f;
+        // with r = 1 / sqrt(...) and wd = w du: dx = r wd - x r^3 mean(wd x)
+        float ss = 0.0f, dot = 0.0f, wd[2 * V];
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) {
+          wd[i] = w[i] * d[i];
           ss += v[i] * v[i];
-          dot += d[i] * w[i] * v[i];
+          dot += wd[i] * v[i];
         }
         ss = head_sum<LPH>(ss);
         dot = head_sum<LPH>(dot);
-        const float r = 1.0f / sqrtf(ss * (1.0f / DH) + a.eps);
-        const float m = r * dot * (1.0f / DH);  // mean of (w du x r)
+        const float r = rsqrtf(ss * (1.0f / DH) + a.eps);
+        const float m = r * r * r * dot * (1.0f / DH);
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) {
-          const float hat = v[i] * r;
-          dw[i] += d[i] * hat;
-          d[i] = r * (w[i] * d[i] - hat * m);
+          dw[i] += d[i] * r * v[i];
+          d[i] = r * wd[i] - v[i] * m;
         }
       }
       if (on && dx) {
@@ -398,6 +400,7 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
      }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!want_dw) return;
   // this block's share of dw: lanes of equal `sub`, then the warps in order
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -421,6 +424,7 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
 __global__ void __launch_bounds__(1024)
 qk_dw_sum_kernel(const float* __restrict__ partial, int nq, int nk, int DH, float* dwq, float* dwk) {
   __shared__ float red[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = DH / 32, part = blockIdx.x / per;
   const int col = (blockIdx.x % per) * 32 + threadIdx.x;
   float* out = part == 0 ? dwq : dwk;
@@ -439,12 +443,6 @@ qk_dw_sum_kernel(const float* __restrict__ partial, int nq, int nk, int DH, floa
   }
 }
 
-// Blocks of a part of `rows` rows in units of hpu heads.
-int part_blocks(long long rows, int heads, int hpu, int upb, int most) {
-  const long long units = rows * cdiv(heads, hpu);
-  const long long n = (units + upb - 1) / upb;
-  return (int)(n < most ? n : most);
-}
 // Heads a unit walks through: all of the row's heads share its cosines and sines, but a
 // small batch spreads its heads over more lanes (148 SMs x 8 warps filled first).
 int heads_per_unit(long long rows, int heads, int lph) {
@@ -452,14 +450,20 @@ int heads_per_unit(long long rows, int heads, int lph) {
 }
 int lanes_per_head(int head_dim, int es) { return head_dim * es / 32; }
 
-void plan(KArgs& g, int head_dim, int es, int most) {
+// All blocks are resident at once and share out the parts' units in proportion.
+void plan(KArgs& g, int head_dim, int es) {
   const QkArgs& a = g.a;
   const int lph = lanes_per_head(head_dim, es), upb = kThreads / lph;
   const int heads = a.q_heads > a.kv_heads ? a.q_heads : a.kv_heads;
   g.hpu = heads_per_unit((long long)a.T * a.kslots, heads, lph);
-  g.nb[0] = a.q ? part_blocks((long long)a.T * a.kslots, a.q_heads, g.hpu, upb, most) : 0;
-  g.nb[1] = a.k ? part_blocks(a.T, a.kv_heads, g.hpu, upb, most) : 0;
-  g.nb[2] = a.v ? part_blocks(a.T, a.kv_heads, g.hpu, upb, most) : 0;
+  const long long rows[3] = {a.q ? (long long)a.T * a.kslots : 0, a.k ? a.T : 0, a.v ? a.T : 0};
+  long long blocks[3], all = 0;
+  for (int p = 0; p < 3; ++p) {
+    blocks[p] = (rows[p] * cdiv(p == 0 ? a.q_heads : a.kv_heads, g.hpu) + upb - 1) / upb;
+    all += blocks[p];
+  }
+  for (int p = 0; p < 3; ++p)
+    g.nb[p] = (int)(all <= kBlocks || blocks[p] == 0 ? blocks[p] : 1 + blocks[p] * (kBlocks - 3) / all);
 }
 
 template <typename T, int DH>
@@ -483,24 +487,31 @@ cudaError_t bwd(const KArgs& g, cudaStream_t s) {
   else qk_bwd_kernel<T, DH, false><<<grid, kThreads, 0, s>>>(g);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!g.a.dwq && !g.a.dwk)) return e;
-  qk_dw_sum_kernel<<<2 * (DH / 32), dim3(32, 32), 0, s>>>(g.a.partial, g.nb[0], g.nb[1], DH,
-                                                          g.a.dwq, g.a.dwk);
-  return cudaGetLastError();
+  // starts early and waits for the shares on the device
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (DH / 32));
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_dw_sum_kernel, (const float*)g.a.partial, g.nb[0], g.nb[1], DH, g.a.dwq,
+                            g.a.dwk);
 }
-
-constexpr int kFwdBlocks = 8 * 148;
 
 }  // namespace
 
 size_t qk_bwd_partial_floats(int T, int kslots, int q_heads, int kv_heads, int head_dim) {
   (void)T; (void)kslots; (void)q_heads; (void)kv_heads;
-  return (size_t)2 * kMaxBlocks * head_dim;
+  return (size_t)kBlocks * head_dim;
 }
 
 cudaError_t launch_qk_fwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s) {
   KArgs g{};
   g.a = a;
-  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4, kFwdBlocks);
+  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4);
   if (dt == SMOE_BF16) return head_dim == 64 ? fwd<bf16, 64>(g, s) : fwd<bf16, 128>(g, s);
   return head_dim == 64 ? fwd<float, 64>(g, s) : fwd<float, 128>(g, s);
 }
@@ -509,14 +520,14 @@ cudaError_t launch_cache_append(const QkArgs& a, cudaStream_t s) {
   KArgs g{};
   g.a = a;
   g.c = *a.cache;
-  plan(g, g.c.head_dim, 2, kFwdBlocks);
+  plan(g, g.c.head_dim, 2);
   return g.c.head_dim == 64 ? append<64>(g, s) : append<128>(g, s);
 }
 
 cudaError_t launch_qk_bwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s) {
   KArgs g{};
   g.a = a;
-  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4, kMaxBlocks);
+  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4);
   if (dt == SMOE_BF16) return head_dim == 64 ? bwd<bf16, 64>(g, s) : bwd<bf16, 128>(g, s);
   return head_dim == 64 ? bwd<float, 64>(g, s) : bwd<float, 128>(g, s);
 }

@@ -48,16 +48,15 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Two scores of one row that differ by more than kApart (1 + |c|) rank as in 64 bits.
-// ex2 and rcp are within 2^-22 and 2^-23 of their value and an exponent x loses 2^-23 |x|,
-// which times exp(-|x|) stays under 2^-23: a sigmoid is within 2^-22.  A softmax's sum of
-// up to 1024 terms (32 in a lane, 5 steps across) adds 2^-18.5 of a score, or of the sum of
-// a group's two best, which is at most 1.  So two such values are within 2^-17.5 of their
-// distance, and a bias added to each costs 2^-23 |c| more.
-constexpr float kApart = 1.0f / (1 << 17);
-__device__ __forceinline__ bool apart(float hi, float lo, float size) {
-  return hi - lo > kApart * (1.0f + size);
-}
+// How far apart two ranks of a row have to be in 32 bits to rank so in 64: kNear times the
+// largest score there can be and kRound times the ranks' size; twice that for the sums of
+// two that groups are ranked by.  ex2 and rcp are within 2^-22 and 2^-23 of their value and
+// an exponent x loses 2^-23 |x|; times s (1 - s) that is under 2^-24 each, with rcp's own
+// and two roundings 2^-22 for a sigmoid, 2^-21 for two.  A softmax is within 2^-18.4 of
+// itself (its sum has up to 1024 terms, 32 in a lane and 5 steps across), two within 2^-17
+// of the largest.  The bias added rounds by 2^-24 of each rank, and the place that takes up
+// to three bits of it moves it by 7 units of 2^-23.
+constexpr float kNearSigmoid = 1.0f / (1 << 21), kNearSoftmax = 1.0f / (1 << 17), kRound = 1.0f / (1 << 20);
 
 // The lane that holds the warp's largest (v, then lowest e) of 64-bit values; e < 0: none.
 __device__ __forceinline__ int best_lane64(double v, int e) {
@@ -168,7 +167,7 @@ __device__ int select_row64(const T* __restrict__ row, const SelectArgs& a, doub
 // from lane 0 on take part.  Renormalised gates divide out the row's largest factor
 // first, so that a row of very negative logits does not lose its sum:
 //   1 / (1 + exp(-l)) = exp(min(l, 0)) / (1 + exp(-|l|)).
-// lse: log-sum-exp of the row (softmax without renormalisation).
+// row_max, row_den: largest logit and sum of the row (softmax without renormalisation).
 template <int W>
 __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b, bool live,
                                          float row_max, float row_den) {
@@ -177,7 +176,7 @@ __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b,
   float w;
   if (!a.renorm) {
     w = !ok ? 0.0f
-            : a.score == SMOE_SCORE_SOFTMAX ? expf(l - row_max) / row_den : 1.0f / (1.0f + expf(-l));
+            : a.score == SMOE_SCORE_SOFTMAX ? __fdividef(expf(l - row_max), row_den) : __fdividef(1.0f, 1.0f + expf(-l));
     return a.scale * w;
   }
   const float top = a.score == SMOE_SCORE_SOFTMAX ? l : fminf(l, 0.0f);
@@ -185,73 +184,157 @@ __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b,
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
   w = ok ? expf(top - m) : 0.0f;
-  if (a.score == SMOE_SCORE_SIGMOID && ok) w /= 1.0f + expf(-fabsf(l));
+  if (a.score == SMOE_SCORE_SIGMOID && ok) w = __fdividef(w, 1.0f + expf(-fabsf(l)));
   float sum = w;
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  return w > 0.0f ? a.scale * (w / sum) : 0.0f;
+  return w > 0.0f ? a.scale * __fdividef(w, sum) : 0.0f;
 }
 
-// One row in 32 bits.  The experts of a group lie in `lpg` lanes (a power of two, one
-// group: the warp), C <= NV neighbours in a lane, so that a group's best are found in
-// log2(lpg) steps and lanes are in the order of the ids.  Returns as select_row64; -2 in
-// every lane if two ranks lie too close together.
+// Logits of this lane's experts as they lie in memory.
 template <typename T, int NV>
-__device__ int select_row32(const T* __restrict__ row, const SelectArgs& a, int lpg, int C, int lane,
-                            float* row_max, float* row_den) {
-  const bool soft = a.score == SMOE_SCORE_SOFTMAX;
-  const int n = a.E / a.groups, group = lane / lpg, in0 = (lane & (lpg - 1)) * C;
-  const int e0 = group * n + in0;
-  const int have = group < a.groups ? min(C, n - in0) : 0;  // this lane's experts
-  float l[NV], c[NV];
+__device__ __forceinline__ void load_experts(const T* __restrict__ at, int have, bool wide, float* l) {
+  constexpr int VB = NV * sizeof(T) < 16 ? NV * sizeof(T) : 16, VE = VB / sizeof(T);  // of a wide load
 #pragma unroll
   for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
-  constexpr int VB = NV * sizeof(T) < 16 ? NV * sizeof(T) : 16;  // bytes of a wide load
-  constexpr int VE = VB / sizeof(T);
-  if (VE > 1 && C == NV && have == NV && ((a.ld | e0) & (VE - 1)) == 0) {
+  if (wide) {
 #pragma unroll
     for (int i = 0; i < NV; i += VE) {
       T w[VE];
-      if (VB == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(row + e0 + i);
-      if (VB == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(row + e0 + i);
-      if (VB == 4) *reinterpret_cast<unsigned*>(w) = *reinterpret_cast<const unsigned*>(row + e0 + i);
+      if (VB == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at + i);
+      if (VB == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at + i);
+      if (VB == 4) *reinterpret_cast<unsigned*>(w) = *reinterpret_cast<const unsigned*>(at + i);
+      if (VB == 2) w[0] = at[i];
 #pragma unroll
       for (int j = 0; j < VE; ++j) l[i + j] = to_f(w[j]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (i < have) l[i] = to_f(row[e0 + i]);
+      if (i < have) l[i] = to_f(at[i]);
+  }
+}
+
+// Where a lane's experts are: those of a group lie in `lpg` lanes (a power of two, one
+// group: the warp), C <= NV neighbours in a lane, so that a group's best are found in
+// log2(lpg) steps and lanes are in the order of the ids.
+struct Lane {
+  int lane, lpg, group, e0, have;
+};
+
+// select_row64 with the row's scores in registers, so that a lane's exponentials overlap (as
+// loops 32 us instead of 27 where one row of a thousand takes this path).
+template <typename T, int NV>
+__device__ __noinline__ int select_row64_wide(const T* __restrict__ row, const SelectArgs& a, const Lane p) {
+  float lf[NV], b[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const float l = i < p.have ? to_f(row[p.e0 + i]) : -INFINITY;
+    lf[i] = usable(l) ? finite_top(l) : -INFINITY;
+    b[i] = a.bias && i < p.have ? a.bias[p.e0 + i] : 0.0f;
+  }
+  const bool soft = a.score == SMOE_SCORE_SOFTMAX;
+  double c[NV];
+  double mx = -INFINITY, den = 1.0;
+  if (soft) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mx = fmax(mx, (double)lf[i]);
+    mx = warp_max64(mx);
+    den = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) den += lf[i] > -INFINITY ? exp((double)lf[i] - mx) : 0.0;
+    den = warp_sum(den);
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) l[i] = usable(l[i]) ? finite_top(l[i]) : -INFINITY;
-  float mx = 0.0f, den = 1.0f;
-  if (soft && (a.bias || a.groups > 1 || !a.renorm)) {
+  for (int i = 0; i < NV; ++i) {
+    const double l = lf[i];
+    const double s = soft ? exp(l - mx) / den : 1.0 / (1.0 + exp(-l));
+    c[i] = i < p.have && lf[i] > -INFINITY && b[i] > -INFINITY ? s + (double)b[i] : -INFINITY;
+  }
+  bool open = p.group < a.groups;
+  if (a.groups > 1) {
+    double v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v2 = fmax(v2, fmin(v1, c[i]));
+      v1 = fmax(v1, c[i]);
+    }
+    for (int off = 1; off < p.lpg; off <<= 1) {
+      const double o1 = __shfl_xor_sync(kFull, v1, off), o2 = __shfl_xor_sync(kFull, v2, off);
+      v2 = fmax(fmin(v1, o1), fmax(v2, o2));
+      v1 = fmax(v1, o1);
+    }
+    const double gs = a.group_top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
+    int ahead = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double o = __shfl_sync(kFull, gs, g * p.lpg);
+      ahead += o > gs || (o == gs && g < p.group);
+    }
+    open = open && ahead < a.top_groups;
+  }
+  unsigned left = open ? (1u << p.have) - 1 : 0;
+  if (!a.bias) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] = lf[i];  // the order of the logits
+  }
+  int mine = -1, be = -1;
+  double bv = 0.0;
+  bool stale = true;
+  for (int j = 0; j < a.k; ++j) {
+    if (stale) {
+      be = -1;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (((left >> i) & 1u) && (be < 0 || c[i] > bv)) { bv = c[i]; be = p.e0 + i; }
+    }
+    __syncwarp();
+    const int src = best_lane64(bv, be), e = __shfl_sync(kFull, be, src);
+    stale = p.lane == src;
+    if (stale) left &= ~(1u << (e - p.e0));
+    if (p.lane == j) mine = e;
+  }
+  return mine;
+}
+
+// One row in 32 bits: l: this lane's logits (usable or -inf), b: its biases (-inf: expert
+// not available).  Returns as select_row64; -2 in every lane if two ranks lie too close
+// together.
+template <typename T, int NV, bool BIAS>
+__device__ __forceinline__ int select_row32(const T* __restrict__ row, const SelectArgs& a, const Lane& p,
+                                            const float* l, const float* b, float* row_max, float* row_den) {
+  const bool soft = a.score == SMOE_SCORE_SOFTMAX;
+  // A rank is an integer in the order of the floats.  Where its low bits are to spare they
+  // hold the place in the lane, the first highest: with scores, whose last bits are not
+  // exact, and with bf16 logits.
+  constexpr bool SORT = NV <= 8, PACK = SORT && (BIAS || sizeof(T) == 2);
+  float c[NV];
+  float mx = 0.0f, inv = 1.0f;
+  if (soft && (BIAS || a.groups > 1 || !a.renorm)) {
     mx = l[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) mx = fmaxf(mx, l[i]);
     mx = warp_max(mx);
-    den = 0.0f;
+    float den = 0.0f;
     if (mx > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) den += ex2((l[i] - mx) * 1.4426950408889634f);
     }
     den = warp_sum(den);
+    inv = rcp(den);
     *row_max = mx;
     *row_den = den;
   }
+  const float near = soft ? kNearSoftmax * fminf(inv, 1.0f) : kNearSigmoid;
   // scores, with the bias; without one what is ranked in the end is the logits
-  if (a.bias || a.groups > 1) {
-    const float inv = rcp(den);
+  if (BIAS || a.groups > 1) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const float s = soft ? ex2((l[i] - mx) * 1.4426950408889634f) * inv
                            : rcp(1.0f + ex2(l[i] * -1.4426950408889634f));
-      const float b = a.bias && i < have ? a.bias[e0 + i] : 0.0f;
-      c[i] = l[i] > -INFINITY && b > -INFINITY ? s + b : -INFINITY;
+      c[i] = l[i] > -INFINITY ? (BIAS ? s + b[i] : s) : -INFINITY;
     }
   }
-  bool open = group < a.groups, close_by = false;
+  bool open = p.group < a.groups, close_by = false;
   if (a.groups > 1) {
     float v1 = -INFINITY, v2 = -INFINITY;
 #pragma unroll
@@ -259,7 +342,7 @@ __device__ int select_row32(const T* __restrict__ row, const SelectArgs& a, int 
       v2 = fmaxf(v2, fminf(v1, c[i]));
       v1 = fmaxf(v1, c[i]);
     }
-    for (int off = 1; off < lpg; off <<= 1) {
+    for (int off = 1; off < p.lpg; off <<= 1) {
       const float o1 = __shfl_xor_sync(kFull, v1, off), o2 = __shfl_xor_sync(kFull, v2, off);
       v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
       v1 = fmaxf(v1, o1);
@@ -267,100 +350,165 @@ __device__ int select_row32(const T* __restrict__ row, const SelectArgs& a, int 
     const float gs = a.group_top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
     int ahead = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const float o = __shfl_sync(kFull, gs, g * lpg);
-      ahead += o > gs || (o == gs && g < group);
+      const float o = __shfl_sync(kFull, gs, g * p.lpg);
+      ahead += o > gs || (o == gs && g < p.group);
     }
     const bool there = open;
     open = open && ahead < a.top_groups;
     if (a.top_groups < a.groups) {
       const float in = warp_min(open ? gs : INFINITY), out = warp_max(there && !open ? gs : -INFINITY);
       const float size = fmaxf(fabsf(v1), v2 > -INFINITY ? fabsf(v2) : 0.0f);
-      close_by = out > -INFINITY && !apart(in, out, warp_max(there && v1 > -INFINITY ? size : 0.0f));
+      const float most = warp_max(there && v1 > -INFINITY ? size : 0.0f);
+      close_by = out > -INFINITY && !(in - out > 2.0f * (near + kRound * most));
     }
   }
-  // unavailable experts rank at -inf, what is not to be chosen is NaN
-  float best = NAN;
+  // INT_MIN: not to be chosen (an unavailable expert's -inf ranks above that)
+  int key[NV], place[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (!a.bias) c[i] = l[i];
-    if (!open || i >= have) c[i] = NAN;
-    best = fmaxf(best, c[i]);
+    const int f = __float_as_int((BIAS ? c[i] : l[i]) + 0.0f);  // -0 is 0
+    const int o = f ^ ((f >> 31) & 0x7fffffff);
+    key[i] = open && i < p.have ? (PACK ? (o & ~7) | (7 - i) : o) : INT_MIN;
+    place[i] = i;
   }
-  const int rounds = a.bias ? a.k + 1 : a.k;  // with scores the next one too, to be compared
-  int mine = -1;
-  float rank = NAN;
-  for (int j = 0; j < rounds; ++j) {
-    const float top = warp_max(best);
-    const unsigned who = __ballot_sync(kFull, best == top);
-    if (who == 0) break;  // no candidate left (only after the k-th)
-    const int src = __ffs(who) - 1;
-    int e = 0;
-    if (lane == src) {
-      bool found = false;
-      best = NAN;
+  // a lane of few experts puts them in order (neighbours change places, so equal ones stay
+  // as they are); one of many looks for its best each time
+  int best = INT_MIN;
+  if (SORT) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (!found && c[i] == top) {
-          found = true;
-          e = e0 + i;
-          c[i] = NAN;
+    for (int r = NV - 1; r > 0; --r)
+#pragma unroll
+      for (int i = 0; i < r; ++i) {
+        const int x = max(key[i], key[i + 1]), y = min(key[i], key[i + 1]);
+        if (!PACK) {
+          const bool swap = key[i + 1] > key[i];
+          const int u = swap ? place[i + 1] : place[i], v = swap ? place[i] : place[i + 1];
+          place[i] = u; place[i + 1] = v;
         }
-        best = fmaxf(best, c[i]);
+        key[i] = x; key[i + 1] = y;
+      }
+    best = key[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+  }
+  const int rounds = BIAS ? a.k + 1 : a.k;  // with scores the next one too, to be compared
+  int mine = -1, rank = INT_MIN;
+  for (int j = 0; j < rounds; ++j) {
+    const int head = PACK ? best & ~7 : best;  // equal ones in two lanes: the first lane's
+    const int top = __reduce_max_sync(kFull, head);
+    if (top == INT_MIN) break;  // no candidate left (only after the k-th)
+    const int src = __ffs(__ballot_sync(kFull, head == top)) - 1;
+    int e = p.e0 + (PACK ? 7 - (best & 7) : place[0]);
+    if (p.lane == src) {
+      if (SORT) {
+#pragma unroll
+        for (int i = 0; i + 1 < NV; ++i) {
+          key[i] = key[i + 1];
+          if (!PACK) place[i] = place[i + 1];
+        }
+        key[NV - 1] = INT_MIN;
+        best = key[0];
+      } else {
+        bool found = false;
+        best = INT_MIN;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (!found && key[i] == top) {
+            found = true;
+            e = p.e0 + i;
+            key[i] = INT_MIN;
+          }
+          best = max(best, key[i]);
+        }
       }
     }
     e = __shfl_sync(kFull, e, src);
-    if (lane == j) {
+    if (p.lane == j) {
       mine = e;
       rank = top;
     }
   }
-  if (a.bias) {
-    const float next = __shfl_down_sync(kFull, rank, 1);
-    float lm = 0.0f, bm = 0.0f;
-    if (mine >= 0) {
-      lm = finite_top(to_f(row[mine]));
-      bm = a.bias[mine];
+  if (BIAS) {
+    const int below = __shfl_down_sync(kFull, rank, 1);
+    const float hi = __int_as_float(rank ^ ((rank >> 31) & 0x7fffffff));
+    const float lo = __int_as_float(below ^ ((below >> 31) & 0x7fffffff));
+    // (a rank of -inf loses its last bits to NaN, no rank is one too: neither is near)
+    const bool near_by = p.lane < a.k && lo > -INFINITY && !(hi - lo > near + kRound * fabsf(hi));
+    if (__any_sync(kFull, near_by)) {  // equal logits and biases are equal in 64 bits as well
+      float lm = 0.0f, bm = 0.0f;
+      if (mine >= 0) {
+        lm = finite_top(to_f(row[mine]));
+        bm = a.bias[mine];
+      }
+      const float ln = __shfl_down_sync(kFull, lm, 1), bn = __shfl_down_sync(kFull, bm, 1);
+      close_by = close_by || (near_by && !(lm == ln && bm == bn));
     }
-    const float ln = __shfl_down_sync(kFull, lm, 1), bn = __shfl_down_sync(kFull, bm, 1);
-    // (a NaN: there is no next one)
-    if (lane < a.k && next > -INFINITY && !apart(rank, next, fabsf(rank)) && !(lm == ln && bm == bn)) close_by = true;
   }
   if (__any_sync(kFull, close_by)) return -2;
-  return lane < a.k ? mine : -1;
+  return p.lane < a.k ? mine : -1;
 }
 
-// One warp per row; lpg = 0: every row in 64 bits.
-template <typename T, int NV>
-__global__ void __launch_bounds__(kWarps * 32)
+// One warp per row, its next row's logits on their way; lpg = 0: every row in 64 bits.
+// The ranking in 64 bits is rare, so it may spill: nine CTAs of the common path fit an SM.
+constexpr int per_sm(int nv) { return nv <= 8 ? 9 : 4; }
+template <typename T, int NV, bool BIAS>
+__global__ void __launch_bounds__(kWarps * 32, per_sm(NV))
 select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int C, int32_t* __restrict__ idx,
               float* __restrict__ gates) {
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= a.T) return;
-  const T* row = logits + (size_t)t * a.ld;
-  float mx = -INFINITY, den = 0.0f;
-  int e = -2;
-  if (lpg > 0) e = select_row32<T, NV>(row, a, lpg, C, lane, &mx, &den);
-  if (e == -2) e = select_row64(row, a, smem + (size_t)warp * (a.E + a.groups), lane);
-  if (lpg == 0 && a.score == SMOE_SCORE_SOFTMAX && !a.renorm) {
-    for (int i = lane; i < a.E; i += 32) {
-      const float l = to_f(row[i]);
-      if (usable(l)) mx = fmaxf(mx, finite_top(l));
-    }
-    mx = warp_max(mx);
-    for (int i = lane; i < a.E; i += 32) {
-      const float l = to_f(row[i]);
-      if (usable(l)) den += expf(finite_top(l) - mx);
-    }
-    den = warp_sum(den);
+  const int n = a.E / a.groups, in0 = lpg ? (lane & (lpg - 1)) * C : 0;
+  Lane p;
+  p.lane = lane;
+  p.lpg = lpg;
+  p.group = lpg ? lane / lpg : 0;
+  p.e0 = p.group * n + in0;
+  p.have = p.group < a.groups && lpg ? max(0, min(C, n - in0)) : 0;
+  constexpr int VE = NV * sizeof(T) < 16 ? NV : 16 / sizeof(T);
+  const bool wide = p.have == NV && ((a.ld | p.e0) & (VE - 1)) == 0;
+  float b[NV], next[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    b[i] = BIAS && i < p.have ? a.bias[p.e0 + i] : 0.0f;
+    if (!(b[i] > -INFINITY)) b[i] = -INFINITY;
   }
-  const float lf = e >= 0 ? to_f(row[e]) : 0.0f;
-  const float b = e >= 0 && a.bias ? a.bias[e] : 0.0f;
-  const float g = gate_of<32>(a, lf, b, e >= 0, mx, den);
-  if (e >= 0) {
-    idx[(size_t)t * a.k + lane] = e;
-    gates[(size_t)t * a.k + lane] = g;
+  const int step = gridDim.x * kWarps;
+  int t = blockIdx.x * kWarps + warp;
+  if (t < a.T && lpg) load_experts<T, NV>(logits + (size_t)t * a.ld + p.e0, p.have, wide, next);
+  for (; t < a.T; t += step) {
+    const T* row = logits + (size_t)t * a.ld;
+    float mx = -INFINITY, den = 0.0f;
+    int e = -2;
+    if (lpg > 0) {
+      float l[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) l[i] = usable(next[i]) ? finite_top(next[i]) : -INFINITY;
+      if (t + step < a.T) load_experts<T, NV>(row + (size_t)step * a.ld + p.e0, p.have, wide, next);
+      e = select_row32<T, NV, BIAS>(row, a, p, l, b, &mx, &den);
+      if (NV <= 8 && e == -2) e = select_row64_wide<T, NV>(row, a, p);
+    }
+    if ((NV > 8 || lpg == 0) && e == -2)
+      e = select_row64(row, a, smem + (size_t)warp * (a.E + a.groups), lane);
+    if (lpg == 0 && a.score == SMOE_SCORE_SOFTMAX && !a.renorm) {
+      for (int i = lane; i < a.E; i += 32) {
+        const float l = to_f(row[i]);
+        if (usable(l)) mx = fmaxf(mx, finite_top(l));
+      }
+      mx = warp_max(mx);
+      for (int i = lane; i < a.E; i += 32) {
+        const float l = to_f(row[i]);
+        if (usable(l)) den += expf(finite_top(l) - mx);
+      }
+      den = warp_sum(den);
+    }
+    const float lf = e >= 0 ? to_f(row[e]) : 0.0f;
+    const float bm = BIAS && e >= 0 ? a.bias[e] : 0.0f;
+    const float g = gate_of<SMOE_MAX_TOPK>(a, lf, bm, e >= 0, mx, den);
+    if (e >= 0) {
+      idx[(size_t)t * a.k + lane] = e;
+      gates[(size_t)t * a.k + lane] = g;
+    }
   }
 }
 
@@ -544,19 +692,22 @@ select_bwd_wide_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t
 template <typename T>
 cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* gates, cudaStream_t s) {
   const size_t smem = (size_t)kWarps * (a.E + a.groups) * sizeof(double);
-  const int grid = cdiv(a.T, kWarps);
   int lpg = a.groups <= 32 ? 32 : 0;
   while (lpg * a.groups > 32) lpg >>= 1;
   const int C = lpg ? cdiv(a.E / a.groups, lpg) : 0;
   // 32 values are what fits a lane's registers beside their scores
-#define SELECT(NV, L) select_kernel<T, NV><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates)
-  if (lpg == 0 || C > 32) SELECT(1, 0);
-  else if (C == 1) SELECT(1, lpg);
-  else if (C == 2) SELECT(2, lpg);
-  else if (C <= 4) SELECT(4, lpg);
-  else if (C <= 8) SELECT(8, lpg);
-  else if (C <= 16) SELECT(16, lpg);
-  else SELECT(32, lpg);
+  // a row for each warp: CTAs come and go while a row is ranked in 64 bits
+#define SELECT(NV, L)                                                                             \
+  const int grid = cdiv(a.T, kWarps);                                                             \
+  a.bias ? select_kernel<T, NV, true><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates) \
+         : select_kernel<T, NV, false><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates)
+  if (lpg == 0 || C > 32) { SELECT(1, 0); }
+  else if (C == 1) { SELECT(1, lpg); }
+  else if (C == 2) { SELECT(2, lpg); }
+  else if (C <= 4) { SELECT(4, lpg); }
+  else if (C <= 8) { SELECT(8, lpg); }
+  else if (C <= 16) { SELECT(16, lpg); }
+  else { SELECT(32, lpg); }
 #undef SELECT
   return cudaGetLastError();
 }

@@ -314,6 +314,27 @@ def test_append_reports_and_skips_bad_places():
     assert torch.equal(kc[0, 0, 0], k[1]) and torch.equal(kc[0, 1, 0], k[2])
 
 
+def test_append_e4m3_of_tiny_and_large_rows():
+    """Rows down to the smallest bf16 number: codes stay finite and within half a step."""
+    kc, vc = _cache(1, 8, 1, 64, True)
+    sc = [torch.ones(1, 8, 1, device="cuda") for _ in range(2)]
+    table = torch.zeros(6, 1, dtype=torch.int32, device="cuda")
+    lens = torch.arange(1, 7, dtype=torch.int32, device="cuda")
+    size = torch.tensor([2.0 ** -133, 1e-38, 1e-30, 1.0, 1e30, 3e38])
+    g = torch.Generator().manual_seed(21)
+    k = (size[:, None] * (0.25 + 0.75 * torch.rand(6, 64, generator=g))).to(BF)
+    smoe.smoe_moa_cache_append(None, k.cuda(), k.cuda(), kc, vc, table, lens, None, 1, 1, norm=False,
+                               k_scale=sc[0], v_scale=sc[1])
+    assert smoe.smoe_check() == 0
+    for c, s in ((kc, sc[0]), (vc, sc[1])):
+        s = s[0, :6].cpu().double()
+        got = c[0, :6, 0].cpu().view(torch.float8_e4m3fn).double() * s
+        want = k.double()
+        # e4m3's half steps, and the fp32 roundings of the scale and its reciprocal
+        tol = (2.0 ** -4 * want + 2.0 ** -10 * s) * (1 + 2.0 ** -20)
+        assert torch.isfinite(got).all() and ((got - want).abs() <= tol).all()
+
+
 def test_graph_and_stream():
     p = _problem("slots", 8)
     q, k, slots = _gpu(p, "q", "k", "slots")
