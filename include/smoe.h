@@ -407,8 +407,9 @@ int smoe_moa_qk_norm_rope_bwd(const smoe_qk_desc* desc, const void* dyq, int64_t
  * workspace: smoe_moa_decode_workspace_size(B, kslots, q_heads, kv_heads, head_dim)
  * bytes, 256-byte aligned; nothing in it is kept between calls.  The sums run in an
  * order fixed by the sizes and lengths: equal calls give equal bits.
- * Both require head_dim 64 or 128, max_pages * page_size <= 2^30, strides that are
- * multiples of 16 bytes (else SMOE_ERR_INVALID_ARG), dtype bf16 (SMOE_ERR_UNSUPPORTED).
+ * Both require head_dim 64 or 128, max_pages * page_size <= 2^30 (smoe_moa_decode: and
+ * B * max_pages * page_size <= 2^34, kslots <= 128), strides that are multiples of 16
+ * bytes below 2^36 (else SMOE_ERR_INVALID_ARG), dtype bf16 (SMOE_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef struct {
   void* k;

@@ -1036,6 +1036,8 @@ int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int 
   if (!slots_fit(c.B, kslots) || (long long)c.B * kslots >= (1LL << 31) / q_heads / c.head_dim)
     return fail(SMOE_ERR_INVALID_ARG, "tensor too large for 32-bit row indexing");
   if (c.B == 0) return SMOE_OK;
+  if ((long long)c.max_pages * c.page_size > (1LL << 34) / c.B)
+    return fail(SMOE_ERR_INVALID_ARG, "B * max_pages * page_size is above 2^34");
   NEED(q, "q"); NEED(o, "o");
   ROWS(q, ldq, (int64_t)q_heads * c.head_dim, 2, "q");
   ALIGNED(o, "o");

@@ -36,6 +36,8 @@
 // a step is at most 2^-8 of each weight, the size of the rounding of the output itself.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "tc_ptx.cuh"
 
 namespace smoe {
@@ -188,10 +190,6 @@ __device__ __forceinline__ void next_unit(Cursor& p, const smoe_kv_cache& c) {
     p.tiles = tiles_in<UNIT>(p.len);
   } while (p.tiles == 0);
 }
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
-
 // Slot and query head of query qi of key head kvh of sequence b.
 __device__ __forceinline__ int query_slot(const DecArgs& a, int b, int qi, int kvh, int* head) {
   *head = kvh * a.group + qi % a.group;
@@ -221,8 +219,8 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   constexpr int R = 8 * NT, KS = DH / 16, H = TL::H, UNIT = TL::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ unsigned masks[kWarps][STAGES];
-  __shared__ long long before[kSpread];  // costs before each run of sequences
-  __shared__ long long wsum[kWarps];
+  __shared__ int before[kSpread];  // costs before each run of sequences (all: below 2^31)
+  __shared__ int wsum[kWarps];
   __shared__ Cursor fifo[kWarps][kFifo];
 
   const smoe_kv_cache& c = a.c;
@@ -232,7 +230,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
 
   // ---- the row of units: costs of the runs of sequences --------------------------
   const int per = (c.B + kSpread - 1) / kSpread;
-  long long mine = 0;
+  int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = threadIdx.x * per + i;
     if (b >= c.B) break;
@@ -241,15 +239,15 @@ decode_kernel(const __grid_constant__ DecArgs a) {
     const int t = tiles_in<UNIT>(seq_len(c, b));
     mine += t > 0 ? t + kItemCost : 0;
   }
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long v = __shfl_up_sync(kFull, incl, off);
+    const int v = __shfl_up_sync(kFull, incl, off);
     if (lane >= off) incl += v;
   }
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) incl += wsum[w];
@@ -259,31 +257,30 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   __syncthreads();
   // costs of a range that is dealt out (nr of them, W jobs), and of one that is fetched
   const int W = a.workers, nr = max(1, W / items);
-  const long long share = quotient(total, nr);
+  const int share = total / nr;
   const bool fetch = share >= 8 * kLeast;
-  const int dealt = fetch ? (int)(share - share / 8) : max(kLeast, (int)share + 1);
-  const long long rest = total - (long long)nr * dealt;  // not above 0 without fetched ranges
-  const int fetched = fetch ? (int)quotient(rest + nr - 1, nr) : 1;
-  const int ranges = nr + (rest > 0 ? (int)quotient(rest + fetched - 1, fetched) : 0);
-  auto start_of = [&](int r) -> long long {
-    return r <= nr ? (long long)r * dealt : (long long)nr * dealt + (long long)(r - nr) * fetched;
-  };
-  auto range_of = [&](long long x) -> int {
-    const long long y = x - (long long)nr * dealt;
-    return (int)(y < 0 ? quotient(x, dealt) : nr + quotient(y, fetched));
+  const int dealt = fetch ? share - share / 8 : max(kLeast, share + 1);
+  const int rest = total - nr * dealt;  // not above 0 without fetched ranges
+  const int fetched = fetch ? cdiv(rest, nr) : 1;
+  const int ranges = nr + (rest > 0 ? cdiv(rest, fetched) : 0);
+  auto start_of = [&](int r) -> int { return r <= nr ? r * dealt : nr * dealt + (r - nr) * fetched; };
+  auto range_of = [&](int x) -> int {
+    const int y = x - nr * dealt;
+    return y < 0 ? x / dealt : nr + y / fetched;
   };
   // The first unit of a job, for a whole warp.
   auto open_job = [&](unsigned job) -> Cursor {
     Cursor p{};
     p.range = job / items;
     p.it = job - p.range * items;
-    const long long x = start_of(p.range), end = min(total, start_of(p.range + 1));
+    if (p.range >= ranges) return p;
+    const int x = start_of(p.range), end = min(total, start_of(p.range + 1));
     if (x >= end) return p;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kSpread / 32; ++i) n += before[i * 32 + lane] <= x;
     const int t = (int)__reduce_add_sync(kFull, n) - 1;
-    int rem = (int)(x - before[t]);
+    int rem = x - before[t];
     for (p.b = t * per;; ++p.b) {
       p.len = seq_len(c, p.b);
       p.tiles = tiles_in<UNIT>(p.len);
@@ -292,7 +289,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       rem -= cost;
     }
     p.tile = max(0, rem - kItemCost);
-    p.left = (int)(end - x) - max(0, kItemCost - rem);
+    p.left = end - x - max(0, kItemCost - rem);
     return p;
   };
   const unsigned jobs = (unsigned)ranges * items;
@@ -723,7 +720,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
           }
         }
       if (slot == 1 && !whole && lane == 0) {
-        const long long here = min(total, start_of(cp.range + 1)) - cp.left;
+        const int here = min(total, start_of(cp.range + 1)) - cp.left;
         a.split[atomicAdd(&a.counts[1], 1u)] =
             make_int4(cp.b, cp.it, cp.range, range_of(here + cp.tiles - 1 - cp.tile));
       }
@@ -892,7 +889,15 @@ cudaError_t run(const DecArgs& a, cudaStream_t s) {
   static_assert(STAGES >= 2, "a ring needs two stages");
   constexpr size_t smem = (size_t)kWarps * STAGES * TL::kStage;
   auto kern = decode_kernel<DH, NT, F8, STAGES, PER_SM>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the attribute belongs to the kernel on a device and stays: set once for each
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (e == cudaSuccess && !(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  }
   if (e == cudaSuccess) e = launch_early(kern, 148 * PER_SM, kThreads, smem, s, a);
   if (e == cudaSuccess) e = launch_early(decode_join_kernel<DH>, 296, 32 * kJoinWarps, 0, s, a, 8 * NT);
   return e;

@@ -100,7 +100,7 @@ def _cache(B=4, kvh=2, dh=128, pages=8, page=16, max_pages=4, f8=False, **kw):
 BAD_CACHES = [
     (dict(page=0), ARG), (dict(max_pages=-1), ARG), (dict(page=1 << 20, max_pages=1 << 12), ARG),
     (dict(dh=96), UNSUPPORTED), (dict(k_scale=0x10000), ARG), (dict(table_stride=3), ARG),
-    (dict(k_page_stride=4), ARG), (dict(v_token_stride=-256), ARG), (dict(f8=True, k_head_stride=8), ARG),
+    (dict(k_page_stride=4), ARG), (dict(v_token_stride=-256), ARG), (dict(k_page_stride=1 << 36), ARG), (dict(f8=True, k_head_stride=8), ARG),
     (dict(seq_lens=None), ARG), (dict(block_table=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG),
     (dict(v=0x10008), ARG)]
 APPEND = dict(desc=_desc(), q=P, ldq=256, k=P, ldk=256, v=P, ldv=256, slots=None, starts=None, freq=P,
@@ -127,7 +127,7 @@ def test_append_refuses(kw, rc):
 
 @pytest.mark.parametrize("kw", [
     dict(kslots=0), dict(kslots=129), dict(q_heads=3), dict(q_heads=0), dict(q=None), dict(o=None),
-    dict(ldq=250), dict(ws=None), dict(wsb=64), dict(ws=V(0x10010)), dict(o=V(0x10004))])
+    dict(cache=_cache(B=64, page=1 << 18, max_pages=1 << 12)), dict(ldq=250), dict(ws=None), dict(wsb=64), dict(ws=V(0x10010)), dict(o=V(0x10004))])
 def test_decode_refuses(kw):
     assert _call(smoe.lib().smoe_moa_decode, DECODE, DECODE, **kw) == ARG
 
