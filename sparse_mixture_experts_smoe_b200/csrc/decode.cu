@@ -32,8 +32,10 @@
 // Keys as rows cost ceil(G/8) 8-column products instead of a 16-row tile padded with
 // empty queries; P^T turns from accumulator to operand layout by movmatrix.
 //
-// P is rounded to bf16 for the second product (bf16 values need a bf16 operand): half
-// a step is at most 2^-8 of each weight, the size of the rounding of the output itself.
+// The second product takes P as two bf16 numbers, the rounded weight and what the rounding
+// left, so that a weight keeps 16 bits (one alone would cost the output as much again as
+// its own rounding; the second product's time is under 1%).  e4m3 values take P times
+// their scales in fp16, whose half step of 2^-11 is small beside the values' own 2^-4.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -79,8 +81,17 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// A whole piece of a row that is read once and should leave L2 first: what the warps hand
+// to the joining kernel stays there (128 sequences of up to 4096 tokens: 99 us, without
+// 103; 24 queries to a key head: 48 and 54).
+__device__ __forceinline__ unsigned long long read_once() {
+  unsigned long long policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void cp_async16_once(uint32_t dst, const void* src, unsigned long long policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -301,6 +312,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES) * TL::kStage;
   const int sub = lane % CH, rr = lane / CH;
   constexpr bool SWZ = TL::kSwizzle;
+  const unsigned long long once = read_once();
   static_assert(!SWZ || RPI == 4, "rows 4 i + rr");
   const uint32_t dst0 = ring + rr * TL::kPitch + (SWZ ? sub ^ rr : sub) * 16;
   // row i * RPI + rr of a stage's part that starts at `part`
@@ -343,10 +355,10 @@ decode_kernel(const __grid_constant__ DecArgs a) {
         if (live == kHalf) {
 #pragma unroll
           for (int i = 0; i < kHalf / RPI; ++i)
-            cp_async16_full(row_at(d, i), at16(ks, (unsigned long long)a.k_token * (i * RPI)));
+            cp_async16_once(row_at(d, i), at16(ks, (unsigned long long)a.k_token * (i * RPI)), once);
 #pragma unroll
           for (int i = 0; i < kHalf / RPI; ++i)
-            cp_async16_full(row_at(d + UNIT * TL::kPitch, i), at16(vs, (unsigned long long)a.v_token * (i * RPI)));
+            cp_async16_once(row_at(d + UNIT * TL::kPitch, i), at16(vs, (unsigned long long)a.v_token * (i * RPI)), once);
         } else {
 #pragma unroll
           for (int i = 0; i < kHalf / RPI; ++i) {
@@ -616,7 +628,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       const uint32_t vb = base + UNIT * TL::kPitch;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        uint32_t pf[NT][2];
+        uint32_t pf[NT][2], pr[NT][2];  // pr: what the rounding of pf left (bf16)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float* w = s[h][t];
@@ -630,8 +642,13 @@ decode_kernel(const __grid_constant__ DecArgs a) {
             pf[t][0] = transpose8(pack_f16(w[0] * vs[h][0], w[1] * vs[h][0]));
             pf[t][1] = transpose8(pack_f16(w[2] * vs[h][1], w[3] * vs[h][1]));
           } else {
-            pf[t][0] = transpose8(pack_bf16(w[0], w[1]));
-            pf[t][1] = transpose8(pack_bf16(w[2], w[3]));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t hi = pack_bf16(w[2 * e], w[2 * e + 1]);
+              pr[t][e] = transpose8(pack_bf16(w[2 * e] - __uint_as_float(hi << 16),
+                                              w[2 * e + 1] - __uint_as_float(hi & 0xffff0000u)));
+              pf[t][e] = transpose8(hi);
+            }
           }
         }
         const uint32_t vh = vb + h * kHalf * TL::kPitch;
@@ -643,7 +660,10 @@ decode_kernel(const __grid_constant__ DecArgs a) {
             uint32_t f[4];
             ldsm4_t(f, chunk(va, 2 * k));
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<false>(oacc[t][k], f, pf[t][0], pf[t][1]);
+            for (int t = 0; t < NT; ++t) {
+              mma16816<false>(oacc[t][k], f, pf[t][0], pf[t][1]);
+              mma16816<false>(oacc[t][k], f, pr[t][0], pr[t][1]);
+            }
           }
         } else {
           const uint32_t va = vh + (lane & 15) * TL::kPitch + ((lane >> 4) ^ (SWZ ? lane & 7 : 0)) * 16;

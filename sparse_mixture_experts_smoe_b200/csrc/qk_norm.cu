@@ -108,24 +108,28 @@ struct KArgs {
   int hpu;          // heads a unit (a group of lanes) walks through
 };
 
+__device__ __forceinline__ int unit_row(int u, int chunks) { return chunks == 1 ? u : u / chunks; }
+
+constexpr int kListed = 512;  // sequences whose starts and lengths a block holds
 // Position (and cache slot) of token t in the serving form.  False: leave the row as
 // it is (padding, or a data error, which is reported).
-__device__ __forceinline__ bool serving_place(const KArgs& g, int t, int* pos, int64_t* page, int* off) {
+__device__ __forceinline__ bool serving_place(const KArgs& g, const int* starts, const int* lens, int t, int* pos,
+                                              int64_t* page, int* off) {
   const smoe_kv_cache& c = g.c;
   int b = t, after = 1;  // rows of the sequence from this one on
   if (g.a.starts) {
-    if (t < g.a.starts[0] || t >= g.a.starts[c.B]) return false;  // rows outside every sequence
+    if (t < starts[0] || t >= starts[c.B]) return false;  // rows outside every sequence
     int lo = 0, hi = c.B - 1;  // the last sequence that starts at or before t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (g.a.starts[mid] <= t) lo = mid; else hi = mid - 1;
+      if (starts[mid] <= t) lo = mid; else hi = mid - 1;
     }
     b = lo;
-    after = g.a.starts[b + 1] - t;
-  } else if (c.seq_lens[b] == 0) {
+    after = starts[b + 1] - t;
+  } else if (lens[b] == 0) {
     return false;  // an unused row of the batch
   }
-  const int len = c.seq_lens[b];
+  const int len = lens[b];
   const long long p = (long long)len - after;
   if (after <= 0 || p < 0 || len > (long long)c.max_pages * c.page_size) {
     report_error(g.a.err, ERRBIT_DATA);
@@ -163,7 +167,7 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
   const float* wp = part == PART_Q ? a.wq : a.wk;
   const bool norm = a.norm && part != PART_V, rot = a.inv_freq && part != PART_V;
   const int sub = threadIdx.x % LPH, chunks = cdiv(heads, g.hpu);
-  const long long units = (long long)rows * chunks;
+  const int units = rows * chunks;  // at most the rows' heads: below 2^31 / head_dim
 
   float w[2 * V];
   unsigned long long fr[V];
@@ -177,13 +181,31 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
     fr[i] = rot ? turn_fraction(a.inv_freq[pair_freq<T, DH, kInter>(sub, i)]) : 0ull;
   }
 
+  __shared__ int listed[kServe ? 2 * kListed + 1 : 1];
+  const int *starts = a.starts, *lens = g.c.seq_lens;
+  if (kServe && starts && g.c.B <= kListed) {  // the search for a row's sequence is a chain of reads
+    for (int i = threadIdx.x; i <= g.c.B; i += kThreads) {
+      listed[i] = starts[i];
+      if (i < g.c.B) listed[g.c.B + 1 + i] = lens[i];
+    }
+    __syncthreads();
+    starts = listed;
+    lens = listed + g.c.B + 1;
+  }
+
   // the loop count is the same for all lanes of a block: the head sums shuffle whole warps
-  const long long first = (long long)blk * UPB, step = (long long)g.nb[part] * UPB;
-  for (long long u0 = first; u0 < units; u0 += step) {
-    const long long u = u0 + threadIdx.x / LPH;
+  const int first = blk * UPB, step = g.nb[part] * UPB;
+  const bool slots = part == PART_Q && a.sorted_slot;
+  int next = first + threadIdx.x / LPH;  // the next unit, and its row's slot
+  int next_slot = slots && next < units ? a.sorted_slot[unit_row(next, chunks)] : 0;
+  for (int u0 = first; u0 < units; u0 += step) {
+    const int u = next;
     bool live = u < units;
-    const int row = live ? (int)(u / chunks) : 0;
-    const int h0 = live ? (int)(u % chunks) * g.hpu : 0;
+    const int row = live ? unit_row(u, chunks) : 0;
+    const int h0 = live ? (u - row * chunks) * g.hpu : 0;
+    const int slot = slots ? next_slot : row;
+    next = u <= units - step ? u + step : units;
+    if (slots && next < units) next_slot = a.sorted_slot[unit_row(next, chunks)];
     const T* xr = x + row * ldx;
     uint4 raw[HB][2];
     auto fetch = [&](int hh) {
@@ -201,15 +223,13 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
     int t = row, pos = 0, off = 0;
     int64_t page = 0;
     if (live && part == PART_Q) {
-      int p = row;
-      if (a.sorted_slot) p = a.sorted_slot[row];
-      if (p < 0 || p >= rows) {
+      if (slot < 0 || slot >= rows) {
         report_error(a.err, ERRBIT_DATA);
         live = false;
       }
-      t = p / a.kslots;
+      t = slot / a.kslots;
     }
-    if (kServe) live = live && serving_place(g, t, &pos, &page, &off);
+    if (kServe) live = live && serving_place(g, starts, lens, t, &pos, &page, &off);
     else if (live && rot) pos = a.positions[t];
     float c[V], s[V];
 #pragma unroll
@@ -302,7 +322,7 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
   const bool want_dw = (part == PART_Q ? a.dwq : a.dwk) != nullptr;
   const bool rot = a.inv_freq != nullptr;
   const int sub = threadIdx.x % LPH, chunks = cdiv(heads, g.hpu);
-  const long long units = (long long)rows * chunks;
+  const int units = rows * chunks;  // at most the rows' heads: below 2^31 / head_dim
 
   float w[2 * V], dw[2 * V];
   unsigned long long fr[V];
@@ -316,12 +336,18 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
     }
     fr[i] = rot ? turn_fraction(a.inv_freq[pair_freq<T, DH, kInter>(sub, i)]) : 0ull;
   }
-  const long long first = (long long)blk * UPB, step = (long long)g.nb[part] * UPB;
-  for (long long u0 = first; u0 < units; u0 += step) {
-    const long long u = u0 + threadIdx.x / LPH;
+  const int first = blk * UPB, step = g.nb[part] * UPB;
+  const bool slots = part == PART_Q && a.sorted_slot;
+  int next = first + threadIdx.x / LPH;  // the next unit, and its row's slot
+  int next_slot = slots && next < units ? a.sorted_slot[unit_row(next, chunks)] : 0;
+  for (int u0 = first; u0 < units; u0 += step) {
+    const int u = next;
     bool live = u < units;
-    const int row = live ? (int)(u / chunks) : 0;
-    const int h0 = live ? (int)(u % chunks) * g.hpu : 0;
+    const int row = live ? unit_row(u, chunks) : 0;
+    const int h0 = live ? (u - row * chunks) * g.hpu : 0;
+    const int slot = slots ? next_slot : row;
+    next = u <= units - step ? u + step : units;
+    if (slots && next < units) next_slot = a.sorted_slot[unit_row(next, chunks)];
     const T* xr = x + row * ldx;
     const T* yr = dy + row * ldy;
     uint4 raw[HB][4];
@@ -344,13 +370,11 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
     fetch(0);
     int t = row;
     if (live && part == PART_Q) {
-      int p = row;
-      if (a.sorted_slot) p = a.sorted_slot[row];
-      if (p < 0 || p >= rows) {
+      if (slot < 0 || slot >= rows) {
         report_error(a.err, ERRBIT_DATA);
         live = false;
       }
-      t = p / a.kslots;
+      t = slot / a.kslots;
     }
     const int pos = live && rot ? a.positions[t] : 0;
     float c[V], s[V];

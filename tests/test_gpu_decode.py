@@ -14,9 +14,9 @@ pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 # Relative error of a weight.  The score is an fp32 sum of 128 products of size at most 40
 # (2^-24 times a tree and a chain of under 16 roundings, 2^-15 of an exponent), ex2 2 ulp;
-# then the weight is rounded to bf16 for a bf16 cache, to fp16 with its scale for e4m3.
+# then the weight is held as two bf16 numbers for a bf16 cache, as fp16 with its scale for e4m3.
 SCORE = 2.0 ** -14
-WEIGHT = {False: 2.0 ** -8 + SCORE, True: 2.0 ** -11 + SCORE}
+WEIGHT = {False: 2.0 ** -16 + SCORE, True: 2.0 ** -11 + SCORE}
 
 CASES = {
     # lens, page, kslots, q_heads, kv_heads, dh, e4m3, layout
