@@ -10,8 +10,8 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
-import struct
 
 import torch
 
@@ -357,63 +357,27 @@ def smoe_moa_attn_bwd(q, k, v, o, lse, dout, sorted_slot, kslots, L, heads, stre
     return dq, dk, dv
 
 
-# ---- calls whose host side counts: decode steps of a few microseconds each -----------
-# Their checks are one expression a tensor, which also gives the address; only where it
-# fails is the reason looked for.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_QK = struct.Struct("8if")      # smoe_qk_desc
-_KV = struct.Struct("6P7q6i")   # smoe_kv_cache
+# ---- calls whose host side counts: the checks of their tensors are compiled (binding.cpp)
+_native = None
 
 
-def _elsewhere(dev, stream):
-    """Whether a call has to change the current device or stream."""
-    return stream is not None or dev != torch.cuda.current_device()
+def _calls():
+    """The compiled checks (built in-tree like the library if missing); raises without them."""
+    global _native
+    if _native is None:
+        lib()
+        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+            from . import build as _build
+            _build.build()
+        _native = importlib.import_module("._binding", __name__)
+    return _native
 
 
 def _scope(t, stream):
-    """Context in which a call on ``t`` runs: ``stream``, whose allocations then belong to
-    it, or the current stream of ``t``'s device."""
-    if stream is None:
-        return torch.cuda.device(t.device)
-    if stream.device != t.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    """``stream`` as the current one, whose allocations then belong to it."""
+    if not isinstance(t, torch.Tensor) or stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are not")
     return torch.cuda.stream(stream)
-
-
-def _refuse(t, name, dtype, shape, dev):
-    _need(t, name, dtype, shape)
-    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-
-
-def _at(t, name, dtype, shape, dev):
-    """Address of a contiguous tensor of this type and shape on device ``dev``."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == dev and t.is_contiguous()):
-        return t.data_ptr()
-    _refuse(t, name, dtype, shape, dev)
-
-
-def _at_opt(t, name, dtype, shape, dev):
-    return None if t is None else _at(t, name, dtype, shape, dev)
-
-
-def _rows(t, name, dtype, shape, dev):
-    """(address, row stride) of a matrix whose rows may lie apart (unit stride inside)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        ld, one = t.stride()
-        if one == 1 or shape[1] <= 1:
-            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
-        raise ValueError(f"{name} must have unit stride inside its rows")
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    _refuse(t.contiguous(), name, dtype, shape, dev)
-
-
-def _matrix(t, name):
-    """(shape, device index) of a CUDA matrix."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
-        raise TypeError(f"{name} must be a CUDA tensor of two dimensions")
-    return t.shape, t.get_device()
 
 
 def _score(name):
@@ -426,65 +390,21 @@ def smoe_route_select(logits, k, bias=None, *, score="softmax", renorm=True, sca
                       top_groups=1, group_top=2, topk_idx=None, gates=None, stream=None):
     """Top-k routing from logits [T, E] (fp32 or bf16; the rows may lie apart): scores,
     selection bias, groups, gates (see smoe.h).  Returns (topk_idx [T, k], gates [T, k])."""
-    (T, E), dev = _matrix(logits, "logits")
-    if _elsewhere(dev, stream):
-        with _scope(logits, stream):
-            return smoe_route_select(logits, k, bias, score=score, renorm=renorm, scale=scale,
-                                     groups=groups, top_groups=top_groups, group_top=group_top,
-                                     topk_idx=topk_idx, gates=gates)
-    dt = _dt(logits)
-    x, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
-    b = _at_opt(bias, "bias", torch.float32, (E,), dev)
-    if topk_idx is None:
-        topk_idx = logits.new_empty((T, k), dtype=torch.int32)
-    if gates is None:
-        gates = logits.new_empty((T, k), dtype=torch.float32)
-    _check(lib().smoe_route_select(x, ld, b, T, E, k, _score(score), 1 if renorm else 0, scale, groups,
-                                   top_groups, group_top, dt,
-                                   _at(topk_idx, "topk_idx", torch.int32, (T, k), dev),
-                                   _at(gates, "gates", torch.float32, (T, k), dev), _raw_stream(dev)))
-    return topk_idx, gates
+    args = (logits, bias, topk_idx, gates, k, _score(score), renorm, scale, groups, top_groups, group_top)
+    if stream is None:
+        return _calls().route_select(*args)
+    with _scope(logits, stream):
+        return _calls().route_select(*args)
 
 
 def smoe_route_select_bwd(logits, topk_idx, gates, dgates, *, score="softmax", renorm=True,
                           scale=1.0, dlogits=None, stream=None):
     """Gradient [T, E] of the logits of smoe_route_select, in their dtype."""
-    (T, E), dev = _matrix(logits, "logits")
-    if _elsewhere(dev, stream):
-        with _scope(logits, stream):
-            return smoe_route_select_bwd(logits, topk_idx, gates, dgates, score=score, renorm=renorm,
-                                         scale=scale, dlogits=dlogits)
-    dt = _dt(logits)
-    x, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
-    (_, k), _ = _matrix(topk_idx, "topk_idx")
-    i = _at(topk_idx, "topk_idx", torch.int32, (T, k), dev)
-    g = _at(gates, "gates", torch.float32, (T, k), dev)
-    dg = _at(dgates, "dgates", torch.float32, (T, k), dev)
-    if dlogits is None:
-        dlogits = logits.new_empty((T, E))
-    _check(lib().smoe_route_select_bwd(x, ld, i, g, dg, T, E, k, _score(score), 1 if renorm else 0, scale,
-                                       dt, _at(dlogits, "dlogits", logits.dtype, (T, E), dev),
-                                       _raw_stream(dev)))
-    return dlogits
-
-
-def _qk_sizes(q, k, kslots, q_heads, kv_heads):
-    """(T, head_dim, one of the tensors, its device) of a call on q rows, k rows or both."""
-    if kslots < 1 or q_heads < 1 or kv_heads < 1:
-        raise ValueError("kslots, q_heads and kv_heads must be at least 1")
-    if k is not None:
-        (T, width), dev = _matrix(k, "k")
-        ref, heads = k, kv_heads
-    elif q is not None:
-        (rows, width), dev = _matrix(q, "q")
-        if rows % kslots:
-            raise ValueError(f"q has {rows} rows, not a multiple of kslots = {kslots}")
-        T, ref, heads = rows // kslots, q, q_heads
-    else:
-        raise ValueError("q and k are both None")
-    if width % heads:
-        raise ValueError(f"rows of {width} values do not divide into {heads} heads")
-    return T, width // heads, ref, dev
+    args = (logits, topk_idx, gates, dgates, dlogits, _score(score), renorm, scale)
+    if stream is None:
+        return _calls().route_select_bwd(*args)
+    with _scope(logits, stream):
+        return _calls().route_select_bwd(*args)
 
 
 def smoe_moa_qk_norm_rope_fwd(q, k, sorted_slot, kslots, *, q_heads, kv_heads, positions=None,
@@ -493,37 +413,12 @@ def smoe_moa_qk_norm_rope_fwd(q, k, sorted_slot, kslots, *, q_heads, kv_heads, p
     """Per-head RMS norm and position rotation of grouped queries q [T*kslots,
     q_heads*head_dim] and keys k [T, kv_heads*head_dim] (either may be None); see smoe.h.
     Rows may lie apart.  Returns (q_out, k_out)."""
-    T, dh, ref, dev = _qk_sizes(q, k, kslots, q_heads, kv_heads)
-    if _elsewhere(dev, stream):
-        with _scope(ref, stream):
-            return smoe_moa_qk_norm_rope_fwd(q, k, sorted_slot, kslots, q_heads=q_heads, kv_heads=kv_heads,
-                                             positions=positions, inv_freq=inv_freq, wq=wq, wk=wk, eps=eps,
-                                             norm=norm, interleaved=interleaved, q_out=q_out, k_out=k_out)
-    dt, code, f32, i32 = ref.dtype, _dt(ref), torch.float32, torch.int32
-    desc = _QK.pack(T, kslots, q_heads, kv_heads, dh, code, 1 if norm else 0, 1 if interleaved else 0, eps)
-    x = y = xo = yo = None
-    ldq = ldk = 0
-    if q is not None:
-        shape = (T * kslots, q_heads * dh)
-        x, ldq = _rows(q, "q", dt, shape, dev)
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        xo = _at(q_out, "q_out", dt, shape, dev)
-    elif q_out is not None:
-        raise ValueError("q_out without its input")
-    if k is not None:
-        shape = (T, kv_heads * dh)
-        y, ldk = _rows(k, "k", dt, shape, dev)
-        if k_out is None:
-            k_out = k.new_empty(shape)
-        yo = _at(k_out, "k_out", dt, shape, dev)
-    elif k_out is not None:
-        raise ValueError("k_out without its input")
-    _check(lib().smoe_moa_qk_norm_rope_fwd(
-        desc, x, ldq, y, ldk, _at_opt(sorted_slot, "sorted_slot", i32, (T * kslots,), dev),
-        _at_opt(positions, "positions", i32, (T,), dev), _at_opt(inv_freq, "inv_freq", f32, (dh // 2,), dev),
-        _at_opt(wq, "wq", f32, (dh,), dev), _at_opt(wk, "wk", f32, (dh,), dev), xo, yo, _raw_stream(dev)))
-    return q_out, k_out
+    args = (q, k, sorted_slot, positions, inv_freq, wq, wk, q_out, k_out, kslots, q_heads, kv_heads, norm,
+            interleaved, eps)
+    if stream is None:
+        return _calls().qk_norm_rope_fwd(*args)
+    with _scope(k if k is not None else q, stream):
+        return _calls().qk_norm_rope_fwd(*args)
 
 
 def smoe_moa_qk_norm_rope_bwd(dq_out, dk_out, q, k, sorted_slot, kslots, *, q_heads, kv_heads,
@@ -531,85 +426,12 @@ def smoe_moa_qk_norm_rope_bwd(dq_out, dk_out, q, k, sorted_slot, kslots, *, q_he
                               interleaved=False, stream=None):
     """Gradients of smoe_moa_qk_norm_rope_fwd: (dq, dk, dwq, dwk); dwq and dwk (fp32) are
     None without their weights, dq and dk without dq_out and dk_out."""
-    T, dh, ref, dev = _qk_sizes(dq_out, dk_out, kslots, q_heads, kv_heads)
-    if _elsewhere(dev, stream):
-        with _scope(ref, stream):
-            return smoe_moa_qk_norm_rope_bwd(dq_out, dk_out, q, k, sorted_slot, kslots, q_heads=q_heads,
-                                             kv_heads=kv_heads, positions=positions, inv_freq=inv_freq,
-                                             wq=wq, wk=wk, eps=eps, norm=norm, interleaved=interleaved)
-    dt, code, f32, i32 = ref.dtype, _dt(ref), torch.float32, torch.int32
-    desc = _QK.pack(T, kslots, q_heads, kv_heads, dh, code, 1 if norm else 0, 1 if interleaved else 0, eps)
-    w1, w2 = _at_opt(wq, "wq", f32, (dh,), dev), _at_opt(wk, "wk", f32, (dh,), dev)
-    dq = dk = dwq = dwk = None
-    dx = dy = x = y = ox = oy = ow = ov = ws = None
-    lddx = lddy = ldx = ldy = nbytes = 0
-    if dq_out is not None:
-        shape = (T * kslots, q_heads * dh)
-        dx, lddx = _rows(dq_out, "dq_out", dt, shape, dev)
-        if norm:
-            x, ldx = _rows(q, "q", dt, shape, dev)
-        dq = dq_out.new_empty(shape)
-        ox = dq.data_ptr()
-        if w1 is not None:
-            dwq = wq.new_empty((dh,))
-            ow = dwq.data_ptr()
-    if dk_out is not None:
-        shape = (T, kv_heads * dh)
-        dy, lddy = _rows(dk_out, "dk_out", dt, shape, dev)
-        if norm:
-            y, ldy = _rows(k, "k", dt, shape, dev)
-        dk = dk_out.new_empty(shape)
-        oy = dk.data_ptr()
-        if w2 is not None:
-            dwk = wk.new_empty((dh,))
-            ov = dwk.data_ptr()
-    if ow is not None or ov is not None:
-        nbytes = lib().smoe_moa_qk_norm_rope_bwd_workspace_size(desc)
-        buf = ref.new_empty(nbytes, dtype=torch.uint8)
-        ws = buf.data_ptr()
-    _check(lib().smoe_moa_qk_norm_rope_bwd(
-        desc, dx, lddx, dy, lddy, x, ldx, y, ldy,
-        _at_opt(sorted_slot, "sorted_slot", i32, (T * kslots,), dev),
-        _at_opt(positions, "positions", i32, (T,), dev), _at_opt(inv_freq, "inv_freq", f32, (dh // 2,), dev),
-        w1, w2, ox, oy, ow, ov, ws, nbytes, _raw_stream(dev)))
-    return dq, dk, dwq, dwk
-
-
-def _page_strides(t, name, dtype, shape, dev):
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        page, token, head, one = t.stride()
-        if one != 1 and shape[3] > 1:
-            raise ValueError(f"{name} must have unit stride inside a head")
-        return t.data_ptr(), page, token, head
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    _refuse(t.contiguous(), name, dtype, shape, dev)
-
-
-def _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, written):
-    """(smoe_kv_cache, B, kv_heads, head_dim) of a paged cache, checked."""
-    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda or k_cache.dim() != 4:
-        raise TypeError("k_cache must be a [num_pages, page_size, kv_heads, head_dim] CUDA tensor")
-    dev, shape = k_cache.get_device(), k_cache.shape
-    pages, page, heads, dh = shape
-    dt = torch.bfloat16 if k_scale is None else torch.uint8
-    k, kp, kt, kh = _page_strides(k_cache, "k_cache", dt, shape, dev)
-    v, vp, vt, vh = _page_strides(v_cache, "v_cache", dt, shape, dev)
-    if written and not (kp and kt and kh and vp and vt and vh):
-        for name, st in (("k_cache", (kp, kt, kh)), ("v_cache", (vp, vt, vh))):
-            if any(st[i] == 0 and shape[i] > 1 for i in range(3)):
-                raise ValueError(f"{name} is written and must not be an expanded tensor")
-    ks = vs = 0
-    if k_scale is not None:
-        ks = _at(k_scale, "k_scale", torch.float32, shape[:3], dev)
-        vs = _at(v_scale, "v_scale", torch.float32, shape[:3], dev)
-    elif v_scale is not None:
-        raise ValueError("k_scale and v_scale go together")
-    (B, max_pages), _ = _matrix(block_table, "block_table")
-    table, ldt = _rows(block_table, "block_table", torch.int32, (B, max_pages), dev)
-    lens = _at(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    return _KV.pack(k, v, ks, vs, table, lens, kp, kt, kh, vp, vt, vh, ldt, pages, page, max_pages, B,
-                    heads, dh), B, heads, dh
+    args = (dq_out, dk_out, q, k, sorted_slot, positions, inv_freq, wq, wk, kslots, q_heads, kv_heads, norm,
+            interleaved, eps)
+    if stream is None:
+        return _calls().qk_norm_rope_bwd(*args)
+    with _scope(dk_out if dk_out is not None else dq_out, stream):
+        return _calls().qk_norm_rope_bwd(*args)
 
 
 def smoe_moa_cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, sorted_slot, kslots,
@@ -620,35 +442,12 @@ def smoe_moa_cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, sort
     store keys and values in the paged cache (bf16, or uint8 e4m3 codes with k_scale and
     v_scale), at the places that seq_lens, block_table and starts give them (see smoe.h).
     Rows of q_out that stand for no token are not written."""
-    cache, B, heads, dh = _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, True)
-    dev = k_cache.get_device()
-    if _elsewhere(dev, stream):
-        with _scope(k_cache, stream):
-            return smoe_moa_cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, sorted_slot,
-                                         kslots, q_heads, starts=starts, inv_freq=inv_freq, wq=wq, wk=wk,
-                                         eps=eps, norm=norm, interleaved=interleaved, k_scale=k_scale,
-                                         v_scale=v_scale, q_out=q_out)
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    (T, _), _ = _matrix(k, "k")
-    y, ldk = _rows(k, "k", bf, (T, heads * dh), dev)
-    z, ldv = _rows(v, "v", bf, (T, heads * dh), dev)
-    x = xo = None
-    ldq = 0
-    if q is not None:
-        shape = (T * kslots, q_heads * dh)
-        x, ldq = _rows(q, "q", bf, shape, dev)
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        xo = _at(q_out, "q_out", bf, shape, dev)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _check(lib().smoe_moa_cache_append(
-        _QK.pack(T, kslots, q_heads, heads, dh, BF16, 1 if norm else 0, 1 if interleaved else 0, eps), x, ldq,
-        y, ldk, z, ldv, _at_opt(sorted_slot, "sorted_slot", i32, (T * kslots,), dev),
-        _at_opt(starts, "starts", i32, (B + 1,), dev), _at_opt(inv_freq, "inv_freq", f32, (dh // 2,), dev),
-        _at_opt(wq, "wq", f32, (dh,), dev), _at_opt(wk, "wk", f32, (dh,), dev), cache, xo,
-        _raw_stream(dev)))
-    return q_out
+    args = (q, k, v, k_cache, v_cache, block_table, seq_lens, sorted_slot, starts, inv_freq, wq, wk, k_scale,
+            v_scale, q_out, kslots, q_heads, norm, interleaved, eps)
+    if stream is None:
+        return _calls().cache_append(*args)
+    with _scope(k_cache, stream):
+        return _calls().cache_append(*args)
 
 
 def smoe_moa_decode(q, k_cache, v_cache, block_table, seq_lens, sorted_slot, kslots, q_heads, *,
@@ -656,26 +455,11 @@ def smoe_moa_decode(q, k_cache, v_cache, block_table, seq_lens, sorted_slot, ksl
     """Attention of the newest token of each sequence over the paged cache (see smoe.h):
     q [B*kslots, q_heads*head_dim] bf16, grouped rows (sorted_slot None: row = slot).
     Returns (o like q, lse [B*kslots, q_heads] fp32)."""
-    cache, B, heads, dh = _kv_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, False)
-    dev = k_cache.get_device()
-    if _elsewhere(dev, stream):
-        with _scope(k_cache, stream):
-            return smoe_moa_decode(q, k_cache, v_cache, block_table, seq_lens, sorted_slot, kslots, q_heads,
-                                   k_scale=k_scale, v_scale=v_scale, o=o, lse=lse)
-    rows, shape = B * kslots, (B * kslots, q_heads * dh)
-    x, ldq = _rows(q, "q", torch.bfloat16, shape, dev)
-    slots = _at_opt(sorted_slot, "sorted_slot", torch.int32, (rows,), dev)
-    if o is None:
-        o = q.new_empty(shape)
-    if lse is None:
-        lse = q.new_empty((rows, q_heads), dtype=torch.float32)
-    nbytes = lib().smoe_moa_decode_workspace_size(B, kslots, q_heads, heads, dh)
-    ws = q.new_empty(nbytes or 1, dtype=torch.uint8)
-    _check(lib().smoe_moa_decode(x, ldq, slots, kslots, q_heads, cache,
-                                 _at(o, "o", torch.bfloat16, shape, dev),
-                                 _at(lse, "lse", torch.float32, (rows, q_heads), dev), ws.data_ptr(), nbytes,
-                                 _raw_stream(dev)))
-    return o, lse
+    args = (q, k_cache, v_cache, block_table, seq_lens, sorted_slot, k_scale, v_scale, o, lse, kslots, q_heads)
+    if stream is None:
+        return _calls().decode(*args)
+    with _scope(k_cache, stream):
+        return _calls().decode(*args)
 
 
 def smoe_quantize_weights_fp8(w, stream=None):

@@ -1,8 +1,9 @@
-"""Build libsmoe.so in-tree with nvcc for sm_100a.
+"""Build libsmoe.so in-tree with nvcc for sm_100a, and the Python module beside it.
 
 Each ``csrc/*.cu`` compiles to an object under ``_build/`` (in parallel, only
 when its source or a header changed), then nvcc links the shared library next to
-this file.  Usage: ``python -m sparse_mixture_experts_smoe_b200.build [--force]``.
+this file.  ``csrc/binding.cpp`` (torch tensors to the C entry points) compiles with
+g++ into ``_binding.so``, which loads the library from its own folder.  Usage: ``python -m sparse_mixture_experts_smoe_b200.build [--force]``.
 """
 from __future__ import annotations
 
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsmoe.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -51,6 +54,28 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_binding(force: bool) -> None:
+    inputs = (BINDING_SRC, os.path.join(INCLUDE, "smoe.h"))
+    if not force and os.path.exists(BINDING) and \
+            os.path.getmtime(BINDING) >= max(os.path.getmtime(p) for p in inputs):
+        return
+    import sysconfig
+
+    import torch
+    cuda, home = os.path.dirname(os.path.dirname(nvcc())), os.path.dirname(torch.__file__)
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+            os.path.join(home, "include"), os.path.join(home, "include/torch/csrc/api/include")]
+    lib = os.path.join(home, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{d}" for d in dirs] + [BINDING_SRC, "-o", tmp, f"-L{PKG}", "-lsmoe", "-Wl,-rpath,$ORIGIN",
+                                       f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+                                       "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with open(os.path.join(BUILD, ".lock"), "w") as lock:
@@ -66,6 +91,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             tmp = LIB + ".tmp"
             subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs, check=True)
             os.replace(tmp, LIB)
+        _build_binding(force)
     return LIB
 
 
