@@ -49,15 +49,19 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kHalf = 16;                    // keys of a product's tile
 constexpr int kItemCost = 2;                 // an item's start and end, in units
-constexpr int kLeast = 4;                    // units of a range, rather than more warps
+constexpr int kLeast = 2;                    // units of a range, rather than more warps
+constexpr int kFetch = 32;                   // units of a warp, from which on an eighth is fetched
 constexpr int kSpread = kThreads;            // runs of sequences that the units are counted for
+constexpr int kMostSlots = 128;              // slots of a token
+constexpr int kDirectRows = 1024;            // rows that are looked for rather than listed first
 constexpr int kFifo = 8;                     // ranges between a warp's loads and its products
 
 struct DecArgs {
   const bf16* q;
   int64_t ldq;
   const int32_t* slots;  // sorted_slot, or null: row = slot
-  const int32_t* inv;    // grouped row of each slot that a row names
+  const int32_t* inv;    // grouped row of each slot that a row names; null: rows are looked for
+  int direct;            // no kernel runs before the decode kernel: nothing is fetched
   smoe_kv_cache c;
   int kslots, q_heads, group, G, mts;  // mts: query tiles of 8 NT rows
   unsigned long long page_mul;         // position / page_size = position * page_mul >> page_shift
@@ -72,8 +76,9 @@ struct DecArgs {
   int workers;         // warps
   float* part_o;       // [jobs][2][rows][DH]
   float* part_ml;      // [jobs][2][rows][2]
-  int4* split;         // [jobs] what several ranges hold: b, item, first and last range
-  unsigned* counts;    // ranges fetched, split items
+  int jobs;
+  int4* split;         // [jobs] what the job starts and does not end: b, item, first and last range (-1)
+  unsigned* fetched;   // jobs fetched
   unsigned* err;
 };
 
@@ -148,14 +153,16 @@ __device__ __forceinline__ void pdl_trigger() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Grouped row of each slot, no range taken and no split item.  Entries of slots that no
-// row names keep what they hold: a reader checks that the row it finds names the slot.
+// Grouped row of each slot, no job fetched and none that starts a split item.  Entries of
+// slots that no row names keep what they hold: a reader checks that the row it finds names
+// the slot.
 __global__ void __launch_bounds__(256)
 decode_prepare_kernel(const int32_t* __restrict__ slots, int rows, int32_t* __restrict__ inv,
-                      unsigned* __restrict__ counts, unsigned* err) {
+                      int4* __restrict__ split, int jobs, unsigned* __restrict__ fetched, unsigned* err) {
   pdl_trigger();
   const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < 2) counts[i] = 0;
+  if (i == 0) *fetched = 0;
+  if (i < jobs) split[i] = make_int4(0, 0, 0, -1);
   if (slots == nullptr || i >= rows) return;
   const int p = slots[i];
   if (p >= 0 && p < rows) inv[p] = i;
@@ -206,21 +213,22 @@ __device__ __forceinline__ int query_slot(const DecArgs& a, int b, int qi, int k
   *head = kvh * a.group + qi % a.group;
   return b * a.kslots + qi / a.group;
 }
-// Place (row * q_heads + head) of that query in o and lse; -1 for a column that stands for
-// no query, and for a slot that no row names (reported).
-__device__ __forceinline__ int query_place(const DecArgs& a, int b, int qi, int kvh) {
-  if (qi >= a.G) return -1;
-  int head;
-  const int slot = query_slot(a, b, qi, kvh, &head);
-  int row = slot;
-  if (a.slots) {
+// Grouped row of a slot, for a whole warp; -1 for a slot that no row names (reported).
+__device__ __forceinline__ int row_of(const DecArgs& a, int slot, int lane) {
+  if (!a.slots) return slot;
+  const int all = a.c.B * a.kslots;
+  int row = -1;
+  if (a.inv) {
     row = a.inv[slot];
-    if (row < 0 || row >= a.c.B * a.kslots || a.slots[row] != slot) {
-      report_error(a.err, ERRBIT_DATA);
-      return -1;
-    }
+    if (row < 0 || row >= all || a.slots[row] != slot) row = -1;
+  } else {
+#pragma unroll 16
+    for (int i = lane; i < all; i += 32)
+      if (a.slots[i] == slot) row = i;
+    row = __reduce_max_sync(kFull, row);
   }
-  return row * a.q_heads + head;
+  if (row < 0 && lane == 0) report_error(a.err, ERRBIT_DATA);
+  return row;
 }
 
 template <int DH, int NT, bool F8, int STAGES, int PER_SM>
@@ -233,6 +241,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   __shared__ int before[kSpread];  // costs before each run of sequences (all: below 2^31)
   __shared__ int wsum[kWarps];
   __shared__ Cursor fifo[kWarps][kFifo];
+  __shared__ int16_t sequence_rows[kWarps][kMostSlots];  // of the slots of the sequence at hand (direct)
 
   const smoe_kv_cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -269,7 +278,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   // costs of a range that is dealt out (nr of them, W jobs), and of one that is fetched
   const int W = a.workers, nr = max(1, W / items);
   const int share = total / nr;
-  const bool fetch = share >= 8 * kLeast;
+  const bool fetch = share >= kFetch && !a.direct;
   const int dealt = fetch ? share - share / 8 : max(kLeast, share + 1);
   const int rest = total - nr * dealt;  // not above 0 without fetched ranges
   const int fetched = fetch ? cdiv(rest, nr) : 1;
@@ -304,6 +313,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
     return p;
   };
   const unsigned jobs = (unsigned)ranges * items;
+  if (a.direct && lane == 0 && cta * kWarps + warp < a.jobs) a.split[cta * kWarps + warp] = make_int4(0, 0, 0, -1);
   Cursor cp = open_job(cta * kWarps + warp);
   Cursor ld = cp;
 
@@ -416,7 +426,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
         if (!more || opened - closed == kFifo) break;
         if (!waited) break;
         unsigned r = 0;
-        if (lane == 0) r = atomicAdd(&a.counts[0], 1u);
+        if (lane == 0) r = atomicAdd(a.fetched, 1u);
         r = __shfl_sync(kFull, r, 0) + W;
         more = r < jobs;
         if (!more) break;
@@ -434,7 +444,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       next_unit<UNIT>(ld, c);
       if (ld.left > 0) page = page_of(ld);
     }
-    if (!waited) {  // from here on: the rows of the slots, and the counts
+    if (!waited) {  // from here on: the rows of the slots, and the count
       pdl_wait();
       waited = true;
       if (cp.left <= 0 && more) continue;
@@ -449,12 +459,23 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       fresh = false;
       t0 = cp.tile;
       const int mt = cp.it % a.mts, kvh = cp.it / a.mts;
+      if (a.slots && !a.inv) {
+        for (int i = lane; i < a.kslots; i += 32) sequence_rows[warp][i] = -1;
+        __syncwarp();
+        const int all = c.B * a.kslots;
+#pragma unroll 16
+        for (int i = lane; i < all; i += 32) {
+          const int of = a.slots[i] - cp.b * a.kslots;
+          if (of >= 0 && of < a.kslots) sequence_rows[warp][of] = (int16_t)i;
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         int head = 0, row = -1;
         if (mt * R + 8 * t + gr < a.G) {
           row = query_slot(a, cp.b, mt * R + 8 * t + gr, kvh, &head);
-          if (a.slots) row = a.inv[row];
+          if (a.slots) row = a.inv ? a.inv[row] : sequence_rows[warp][row - cp.b * a.kslots];
           if (row >= c.B * a.kslots) row = -1;
         }
         const bf16* qr = a.q + (row < 0 ? 0 : (int64_t)row * a.ldq + (int64_t)head * DH);
@@ -708,8 +729,17 @@ decode_kernel(const __grid_constant__ DecArgs a) {
           v += __shfl_xor_sync(kFull, v, 16);
           if (mt * R + n >= a.G) continue;
           if (whole) {
-            const int place = query_place(a, cp.b, mt * R + n, kvh);
-            if (place < 0) continue;
+            int head;
+            const int sl = query_slot(a, cp.b, mt * R + n, kvh, &head);
+            int row = sl;
+            if (a.slots) {
+              row = a.inv ? a.inv[sl] : sequence_rows[warp][sl - cp.b * a.kslots];
+              if (row < 0 || row >= c.B * a.kslots || (a.inv && a.slots[row] != sl)) {
+                report_error(a.err, ERRBIT_DATA);
+                continue;
+              }
+            }
+            const int place = row * a.q_heads + head;
             const float inv = v == 0.0f ? 0.0f : 1.0f / v;
             bf16* o = a.o + (int64_t)place * DH;
 #pragma unroll
@@ -741,7 +771,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
         }
       if (slot == 1 && !whole && lane == 0) {
         const int here = min(total, start_of(cp.range + 1)) - cp.left;
-        a.split[atomicAdd(&a.counts[1], 1u)] =
+        a.split[cp.range * items + cp.it] =
             make_int4(cp.b, cp.it, cp.range, range_of(here + cp.tiles - 1 - cp.tile));
       }
       fresh = true;
@@ -751,11 +781,13 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   // sequences without a cached token: o = 0, lse = -inf
   for (int b = cta; b < c.B; b += gridDim.x) {
     if (seq_len(c, b) > 0) continue;
-    for (int i = threadIdx.x; i < a.G * c.kv_heads * (DH / 8); i += kThreads) {
-      const int place = query_place(a, b, i / (DH / 8) % a.G, i / (DH / 8) / a.G);
-      if (place < 0) continue;
-      *reinterpret_cast<uint4*>(a.o + (int64_t)place * DH + 8 * (i % (DH / 8))) = make_uint4(0, 0, 0, 0);
-      if (a.lse && i % (DH / 8) == 0) a.lse[place] = -INFINITY;
+    for (int j = warp; j < a.kslots; j += kWarps) {
+      const int row = row_of(a, b * a.kslots + j, lane);
+      if (row < 0) continue;
+      for (int i = lane; i < a.q_heads * (DH / 8); i += 32)
+        *reinterpret_cast<uint4*>(a.o + (int64_t)row * a.q_heads * DH + 8 * i) = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = lane; i < a.q_heads; i += 32) a.lse[(int64_t)row * a.q_heads + i] = -INFINITY;
     }
   }
   pdl_trigger();
@@ -821,36 +853,57 @@ __device__ __forceinline__ Joined<DH> join_shares(const DecArgs& a, int it, int 
 template <int DH>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 decode_join_kernel(const __grid_constant__ DecArgs a, int R) {
-  constexpr int N = DH / 32;
+  constexpr int N = DH / 32, kListed = 256;
   __shared__ float2 ml[kJoinWarps];
   __shared__ float sums[kJoinWarps][DH];
+  __shared__ int listed[kListed], n_listed;  // this CTA's rows of many shares
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pitch = min(R, a.G);
+  if (threadIdx.x == 0) n_listed = 0;
+  __syncthreads();
   pdl_wait();
-  const int all = (int)a.counts[1] * pitch, step = kJoinWarps * gridDim.x;
-  bool many = false;
-  for (int u = warp * gridDim.x + blockIdx.x; u < all; u += step) {
-    const int4 d = a.split[u / pitch];
-    const int n = u % pitch, mt = d.y % a.mts, kvh = d.y / a.mts;
-    if (mt * R + n >= a.G) continue;
-    if (d.w - d.z >= kFew) {
-      many = true;
-      continue;
-    }
-    const int place = query_place(a, d.x, mt * R + n, kvh);
-    const Joined<DH> r = join_shares<DH>(a, d.y, d.z, d.w, n, pitch, 0, 1, lane);
-    const float inv = r.sum == 0.0f ? 0.0f : 1.0f / r.sum;
-    if (place < 0) continue;
+  // place of row n of a split item, -1: none
+  auto place_of = [&](const int4& d, int n) -> int {
+    int head;
+    const int slot = query_slot(a, d.x, d.y % a.mts * R + n, d.y / a.mts, &head);
+    const int row = row_of(a, slot, lane);
+    return row < 0 ? -1 : row * a.q_heads + head;
+  };
+  // a lane looks at every 32nd of its warp's rows, the warp joins what they find
+  const int all = a.jobs * pitch, step = kJoinWarps * gridDim.x, u0 = warp * gridDim.x + blockIdx.x;
+  for (int base = u0; base < all; base += 32 * step) {
+    int4 e = make_int4(0, 0, 0, -1);
+    const int at = base + lane * step;
+    if (at < all) e = a.split[at / pitch];
+    unsigned todo = __ballot_sync(kFull, e.w >= 0 && e.y % a.mts * R + at % pitch < a.G);
+    for (; todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1, u = base + from * step, n = u % pitch;
+      const int4 d = make_int4(__shfl_sync(kFull, e.x, from), __shfl_sync(kFull, e.y, from),
+                               __shfl_sync(kFull, e.z, from), __shfl_sync(kFull, e.w, from));
+      if (d.w - d.z >= kFew) {
+        int slot = 0;
+        if (lane == 0) slot = atomicAdd(&n_listed, 1);
+        slot = __shfl_sync(kFull, slot, 0);
+        if (slot < kListed) {
+          if (lane == 0) listed[slot] = u;
+          continue;
+        }
+      }
+      const int place = place_of(d, n);
+      const Joined<DH> r = join_shares<DH>(a, d.y, d.z, d.w, n, pitch, 0, 1, lane);
+      if (place < 0) continue;
+      const float inv = r.sum == 0.0f ? 0.0f : 1.0f / r.sum;
 #pragma unroll
-    for (int k = 0; k < N; ++k) a.o[(int64_t)place * DH + 32 * k + lane] = __float2bfloat16_rn(r.v[k] * inv);
-    if (a.lse && lane == 0)
-      a.lse[place] = r.sum == 0.0f ? -INFINITY : (log2f(r.sum) + r.top) * 0.6931471805599453f;
+      for (int k = 0; k < N; ++k) a.o[(int64_t)place * DH + 32 * k + lane] = __float2bfloat16_rn(r.v[k] * inv);
+      if (a.lse && lane == 0)
+        a.lse[place] = r.sum == 0.0f ? -INFINITY : (log2f(r.sum) + r.top) * 0.6931471805599453f;
+    }
   }
-  if (!__syncthreads_or(many)) return;
-  for (int u = blockIdx.x; u < all; u += gridDim.x) {
+  __syncthreads();
+  const int many = min(n_listed, kListed);
+  for (int i = 0; i < many; ++i) {
+    const int u = listed[i], n = u % pitch;
     const int4 d = a.split[u / pitch];
-    const int n = u % pitch, mt = d.y % a.mts, kvh = d.y / a.mts;
-    if (d.w - d.z < kFew || mt * R + n >= a.G) continue;
     const Joined<DH> r = join_shares<DH>(a, d.y, d.z, d.w, n, pitch, warp, kJoinWarps, lane);
     if (lane == 0) ml[warp] = make_float2(r.top, r.sum);
 #pragma unroll
@@ -866,7 +919,7 @@ decode_join_kernel(const __grid_constant__ DecArgs a, int R) {
         sum += f * ml[w].y;
         v += f * sums[w][threadIdx.x];
       }
-      const int place = query_place(a, d.x, mt * R + n, kvh);
+      const int place = place_of(d, n);
       if (place >= 0) {
         a.o[(int64_t)place * DH + threadIdx.x] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : v / sum);
         if (a.lse && threadIdx.x == 0)
@@ -884,12 +937,12 @@ int tiles_of(int G) { return G <= 8 ? 1 : G <= 16 ? 2 : G <= 24 ? 3 : 4; }
 // CTAs on each of 148 SMs: three where the registers allow it (8 queries), else two.
 int workers_of(int nt) { return 148 * kWarps * (nt == 1 ? 3 : 2); }
 
-// Starts while the kernel before it still runs, and waits for it on the device.
+// early: starts while the kernel before it still runs, and waits for it on the device.
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch(bool early, void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
+  at.val.programmaticStreamSerializationAllowed = early;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -918,8 +971,8 @@ cudaError_t run(const DecArgs& a, cudaStream_t s) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   }
-  if (e == cudaSuccess) e = launch_early(kern, 148 * PER_SM, kThreads, smem, s, a);
-  if (e == cudaSuccess) e = launch_early(decode_join_kernel<DH>, 296, 32 * kJoinWarps, 0, s, a, 8 * NT);
+  if (e == cudaSuccess) e = launch(!a.direct, kern, 148 * PER_SM, kThreads, smem, s, a);
+  if (e == cudaSuccess) e = launch(true, decode_join_kernel<DH>, 296, 32 * kJoinWarps, 0, s, a, 8 * NT);
   return e;
 }
 template <int DH, bool F8>
@@ -933,18 +986,18 @@ cudaError_t run_nt(const DecArgs& a, cudaStream_t s) {
 }
 
 struct DecWorkspace {
-  int workers;
-  size_t part_o, part_ml, split, counts, inv, bytes;
+  int workers, jobs;
+  size_t part_o, part_ml, split, fetched, inv, bytes;
   DecWorkspace(int rows, int kv_heads, int G, int head_dim) {
     const int nt = tiles_of(G), items = kv_heads * cdiv(G, 8 * nt);
     workers = workers_of(nt);
-    const size_t jobs = (size_t)2 * (workers > items ? workers : items);
-    const size_t share_rows = jobs * 2 * (G < 8 * nt ? G : 8 * nt);
+    jobs = 2 * (workers > items ? workers : items);
+    const size_t share_rows = (size_t)jobs * 2 * (G < 8 * nt ? G : 8 * nt);
     part_o = 0;
     part_ml = part_o + share_rows * head_dim * 4;
     split = (part_ml + share_rows * 2 * 4 + 15) / 16 * 16;
-    counts = split + jobs * sizeof(int4);
-    inv = counts + 16;
+    fetched = split + (size_t)jobs * sizeof(int4);
+    inv = fetched + 16;
     bytes = inv + (size_t)rows * 4;
   }
 };
@@ -991,13 +1044,24 @@ cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, co
   a.part_ml = (float*)(base + w.part_ml);
   a.workers = w.workers;
   a.split = (int4*)(base + w.split);
-  a.counts = (unsigned*)(base + w.counts);
+  a.fetched = (unsigned*)(base + w.fetched);
   a.inv = (int32_t*)(base + w.inv);
   a.err = err;
-  decode_prepare_kernel<<<cdiv(sorted_slot ? rows : 1, 256), 256, 0, s>>>(sorted_slot, rows, (int32_t*)a.inv,
-                                                                          a.counts, err);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // Without a kernel before it where no batch that the tables can hold has work to fetch, and
+  // its rows are few enough to be looked for (one sequence of 2048 tokens: 9 us, with it 12).
+  const int items = c.kv_heads * a.mts, nr = a.workers / items;
+  const long long most = (long long)c.B * (cdiv(c.max_pages * c.page_size, kHalf) + kItemCost);
+  a.direct = nr >= 1 && most / nr < kFetch && (!sorted_slot || rows <= kDirectRows);
+  a.jobs = a.direct ? nr * items : w.jobs;
+  if (a.direct) {
+    a.inv = nullptr;
+  } else {
+    const int n = sorted_slot && rows > w.jobs ? rows : w.jobs;
+    decode_prepare_kernel<<<cdiv(n, 256), 256, 0, s>>>(sorted_slot, rows, (int32_t*)a.inv, a.split, w.jobs,
+                                                       a.fetched, err);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (c.k_scale)
     return c.head_dim == 64 ? run_nt<64, true>(a, s) : run_nt<128, true>(a, s);
   return c.head_dim == 64 ? run_nt<64, false>(a, s) : run_nt<128, false>(a, s);

@@ -176,7 +176,7 @@ __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b,
   float w;
   if (!a.renorm) {
     w = !ok ? 0.0f
-            : a.score == SMOE_SCORE_SOFTMAX ? __fdividef(expf(l - row_max), row_den) : __fdividef(1.0f, 1.0f + expf(-l));
+            : a.score == SMOE_SCORE_SOFTMAX ? expf(l - row_max) / row_den : 1.0f / (1.0f + expf(-l));
     return a.scale * w;
   }
   const float top = a.score == SMOE_SCORE_SOFTMAX ? l : fminf(l, 0.0f);
@@ -184,11 +184,11 @@ __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b,
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
   w = ok ? expf(top - m) : 0.0f;
-  if (a.score == SMOE_SCORE_SIGMOID && ok) w = __fdividef(w, 1.0f + expf(-fabsf(l)));
+  if (a.score == SMOE_SCORE_SIGMOID && ok) w /= 1.0f + expf(-fabsf(l));
   float sum = w;
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  return w > 0.0f ? a.scale * __fdividef(w, sum) : 0.0f;
+  return w > 0.0f ? a.scale * (w / sum) : 0.0f;
 }
 
 // Logits of this lane's experts as they lie in memory.

@@ -121,15 +121,18 @@ def decode(q, k_cache, v_cache, table, lens, sorted_slot, kslots, q_heads):
     lse = torch.full((rows, q_heads), NEG, dtype=torch.float64)
     slot = torch.arange(rows) if sorted_slot is None else sorted_slot.cpu().long()
     kd, vd, qd = k_cache.double(), v_cache.double(), q.cpu().double().view(rows, q_heads, dh)
+    held = {}  # keys and values of a sequence
     for i in range(rows):
         b = int(slot[i]) // kslots
-        n = min(max(int(lens[b]), 0), table.shape[1] * page)
-        ids = [(int(table[b, u // page]), u % page) for u in range(n)]
-        ids = [(p, f) for p, f in ids if 0 <= p < pages]
-        if not ids:
+        if b not in held:
+            n = min(max(int(lens[b]), 0), table.shape[1] * page)
+            u = torch.arange(n)
+            p_, f_ = table[b][u // page].long(), u % page
+            there = (p_ >= 0) & (p_ < pages)
+            held[b] = kd[p_[there], f_[there]], vd[p_[there], f_[there]]  # [n, kvh, dh]
+        K, V = held[b]
+        if K.shape[0] == 0:
             continue
-        p_, f_ = (torch.tensor(x) for x in zip(*ids))
-        K, V = kd[p_, f_], vd[p_, f_]  # [n, kvh, dh]
         for h in range(q_heads):
             sc = K[:, h // group] @ qd[i, h] / math.sqrt(dh)
             z = torch.logsumexp(sc, 0)
