@@ -10,7 +10,12 @@
 // the lower id.  One warp has a row.  It ranks in 32 bits with scores whose error is
 // bounded, and where two ranks that decide the outcome lie closer together than that
 // bound (and are not equal because logit and bias are), it ranks the row again in 64 bits.
-// Logits of a normal distribution bring that about in under one row of a hundred.
+// Logits of a normal distribution bring that about in one row of a thousand.
+//
+// Bound: instructions.  16384 rows of 256 fp32 logits are 18 MB, 2.8 us at the copy rate;
+// they take 27 us, about 1000 instructions a row: 490 to load, score, order and write, 36
+// for each of the nine rounds, 208 for the groups (16384 x 256 without bias and groups,
+// k = 1: 13 us), and what the few rows in 64 bits add at the end, about 6 us.
 #include <cfloat>
 #include <climits>
 
@@ -696,9 +701,12 @@ cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* ga
   while (lpg * a.groups > 32) lpg >>= 1;
   const int C = lpg ? cdiv(a.E / a.groups, lpg) : 0;
   // 32 values are what fits a lane's registers beside their scores
-  // a row for each warp: CTAs come and go while a row is ranked in 64 bits
+  // One row for each warp, so that CTAs come and go while a row is ranked in 64 bits (16384
+  // rows of 256 experts in groups: 27 us, with several rows a warp 31); with many experts
+  // a lane several, whose logits are asked for a row ahead (1024 experts: 119 us against 135).
 #define SELECT(NV, L)                                                                             \
-  const int grid = cdiv(a.T, kWarps);                                                             \
+  const int rows = NV <= 8 ? 1 : cdiv(a.T, 148 * per_sm(NV) * kWarps);                            \
+  const int grid = cdiv(a.T, kWarps * rows);                                                      \
   a.bias ? select_kernel<T, NV, true><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates) \
          : select_kernel<T, NV, false><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates)
   if (lpg == 0 || C > 32) { SELECT(1, 0); }
