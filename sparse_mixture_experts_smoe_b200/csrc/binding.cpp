@@ -7,6 +7,7 @@
 #include <ATen/core/Tensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -110,8 +111,10 @@ std::pair<Tensor, Tensor> route_select(const Tensor& logits, const OptTensor& bi
   const On on(logits);
   const int64_t T = logits.size(0), E = logits.size(1);
   const Rows x = rows_of(logits, "logits", logits.scalar_type(), T, E, on.dev);
-  if (k < 1) value_error("k must be at least 1");
   const float* b = opt<float>(bias, "bias", F32, {E}, on.dev);
+  if (k < 1 || k > SMOE_MAX_TOPK)  // refused before outputs of that size are made
+    check(smoe_route_select(x.p, as_int(x.ld, "the row stride of logits"), b, as_int(T, "T"), as_int(E, "E"), k, score,
+                            renorm, scale, groups, top_groups, group_top, dt, nullptr, nullptr, nullptr));
   const int64_t shape[2] = {T, k};
   void* i = out(idx, "topk_idx", I32, shape, on.dev);
   void* g = out(gates, "gates", F32, shape, on.dev);
@@ -338,11 +341,13 @@ std::pair<Tensor, Tensor> decode(const Tensor& q, const Tensor& k_cache, const T
 
 }  // namespace
 
+// torch's own errors (out of memory, a lost device) reach Python as torch's classes.
+#define DEF(name) m.def(#name, torch::wrap_pybind_function(name))
 PYBIND11_MODULE(_binding, m) {
-  m.def("route_select", &route_select);
-  m.def("route_select_bwd", &route_select_bwd);
-  m.def("qk_norm_rope_fwd", &qk_norm_rope_fwd);
-  m.def("qk_norm_rope_bwd", &qk_norm_rope_bwd);
-  m.def("cache_append", &cache_append);
-  m.def("decode", &decode);
+  DEF(route_select);
+  DEF(route_select_bwd);
+  DEF(qk_norm_rope_fwd);
+  DEF(qk_norm_rope_bwd);
+  DEF(cache_append);
+  DEF(decode);
 }
