@@ -13,13 +13,21 @@
 // share a head; the mean is log2 of that many shuffles.  A lane keeps its row's cosines
 // and sines for all heads of the row.
 //
-// A lane asks for the pieces of kBatch heads before it uses the first, and for a row's
-// pieces before its position: outputs may be the inputs, so the compiler does not move
-// loads across stores by itself.
+// Forward, a lane asks for the pieces of kBatch heads before it uses the first, and for a
+// row's pieces before its position; backward, for the next head's (the next row's after a
+// row's last) before it uses those at hand.  Outputs may be the inputs, so the compiler
+// does not move loads across stores by itself.
 //
 // Angles: far positions need more than fp32.  inv_freq / (2 pi) is held as a 64-bit
 // fixed-point fraction of a turn, so position * fraction modulo 2^64 is the angle with
-// whole turns dropped exactly; its upper 32 bits go to sincospif.
+// whole turns dropped exactly; its upper 32 bits go to sincospif (bf16: to sin.approx).
+//
+// Bound: the instructions of a pass over 84 MB (8192 tokens, 4 slots, 4 heads of 128 bf16;
+// 13 us at the copy rate): 14 us from L2, 20 from DRAM.  Two fp32 values to an instruction
+// took the forward from 15.1 to 14.0 us, one wave of 296 blocks instead of 1280 from 20.5
+// to 15.9, asking for four heads before the first is used from 28.6 to 20.5.  The backward
+// (126 MB, 19.5 us) takes 32 us: 128 registers a thread leave 16 warps on an SM, each with
+// one head ahead, which is about half of the reads in flight that the memory's rate needs.
 #include "tc_ptx.cuh"
 
 namespace smoe {
@@ -35,16 +43,52 @@ struct Geo {
   static constexpr int kBatch = 4;          // heads loaded ahead, forward
 };
 
-__device__ __forceinline__ void unpack_piece(const uint4& u, float* v, const float*) {
-  v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
-  v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+// Two neighbouring fp32 values in one register pair: products and sums of both in one
+// instruction, which halves what bounds these kernels.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-__device__ __forceinline__ void unpack_piece(const uint4& u, float* v, const bf16*) { unpack8(u, v); }
-__device__ __forceinline__ void store_piece(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ float2 halves(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
 }
-__device__ __forceinline__ void store_piece(bf16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = pack8(v);
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void unpack_piece(const uint4& u, f2* v, const float*) {
+  v[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
+  v[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ void unpack_piece(const uint4& u, f2* v, const bf16*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void store_piece(float* p, const f2* v) {
+  const float2 a = halves(v[0]), b = halves(v[1]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store_piece(bf16* p, const f2* v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = halves(v[i]);
+    f[2 * i] = h.x;
+    f[2 * i + 1] = h.y;
+  }
+  *reinterpret_cast<uint4*>(p) = pack8(f);
 }
 
 template <int LPH>
@@ -86,15 +130,51 @@ __device__ __forceinline__ int pair_freq(int sub, int i) {
   if (!kInter) return sub * V + i;
   return i < V / 2 ? sub * (V / 2) + i : DH / 4 + sub * (V / 2) + i - V / 2;
 }
+// Cosines and sines of the lane's V pairs, and minus the sines (in the order of the values
+// when pairs are halves apart).
+template <int V>
+struct Turn {
+  f2 c[V / 2], s[V / 2], n[V / 2];
+};
+template <typename T, int V>
+__device__ __forceinline__ void turns(const unsigned long long* fr, bool rot, int pos, float sign, Turn<V>& t) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    float c0 = 1.0f, s0 = 0.0f, c1 = 1.0f, s1 = 0.0f;
+    if (rot) {
+      turn<T>(fr[2 * i], pos, &c0, &s0);
+      turn<T>(fr[2 * i + 1], pos, &c1, &s1);
+    }
+    t.c[i] = pair(c0, c1);
+    t.s[i] = pair(sign * s0, sign * s1);
+    t.n[i] = pair(-sign * s0, -sign * s1);
+  }
+}
 // Turns the lane's 2V values x (first V: piece a, last V: piece b) by its V pairs.
 template <int V, bool kInter>
-__device__ __forceinline__ void rotate(float* x, const float* c, const float* s, float sign) {
+__device__ __forceinline__ void rotate(f2* x, const Turn<V>& t) {
+  if (!kInter) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int p = kInter ? 2 * i : i, q = kInter ? 2 * i + 1 : V + i;
-    const float a = x[p], b = x[q], sn = sign * s[i];
-    x[p] = a * c[i] - b * sn;
-    x[q] = b * c[i] + a * sn;
+    for (int i = 0; i < V / 2; ++i) {
+      const f2 a = x[i], b = x[V / 2 + i];
+      x[i] = fma2(b, t.n[i], mul2(a, t.c[i]));
+      x[V / 2 + i] = fma2(a, t.s[i], mul2(b, t.c[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 c = halves(t.c[i / 2]), s = halves(t.s[i / 2]), v = halves(x[i]);
+      const float ci = i % 2 ? c.y : c.x, si = i % 2 ? s.y : s.x;
+      x[i] = pair(v.x * ci - v.y * si, v.y * ci + v.x * si);
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_weights(const float* wp, int at_a, int at_b, f2* w) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    w[i] = wp ? pair(wp[at_a + 2 * i], wp[at_a + 2 * i + 1]) : pair(1.0f, 1.0f);
+    w[V / 2 + i] = wp ? pair(wp[at_b + 2 * i], wp[at_b + 2 * i + 1]) : pair(1.0f, 1.0f);
   }
 }
 
@@ -169,15 +249,11 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
   const int sub = threadIdx.x % LPH, chunks = cdiv(heads, g.hpu);
   const int units = rows * chunks;  // at most the rows' heads: below 2^31 / head_dim
 
-  float w[2 * V];
+  f2 w[V];
+  load_weights<V>(norm ? wp : nullptr, sub * V, DH / 2 + sub * V, w);
   unsigned long long fr[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    w[i] = w[V + i] = 1.0f;
-    if (norm && wp) {
-      w[i] = wp[sub * V + i];
-      w[V + i] = wp[DH / 2 + sub * V + i];
-    }
     fr[i] = rot ? turn_fraction(a.inv_freq[pair_freq<T, DH, kInter>(sub, i)]) : 0ull;
   }
 
@@ -231,75 +307,78 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
     }
     if (kServe) live = live && serving_place(g, starts, lens, t, &pos, &page, &off);
     else if (live && rot) pos = a.positions[t];
-    float c[V], s[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      c[i] = 1.0f; s[i] = 0.0f;
-      if (rot) turn<T>(fr[i], pos, &c[i], &s[i]);
-    }
+    Turn<V> cs;
+    turns<T, V>(fr, rot, pos, 1.0f, cs);
     for (int h4 = 0; h4 < g.hpu; h4 += HB) {
-     if (h4 > 0) fetch(h4);
+      if (h4 > 0) fetch(h4);
 #pragma unroll
-     for (int j = 0; j < HB; ++j) {
-      const int hh = h4 + j;
-      if (hh >= g.hpu) break;
-      const int h = h0 + hh;
-      const bool on = live && h < heads;
-      float v[2 * V];
-      unpack_piece(raw[j][0], v, (const T*)nullptr);
-      unpack_piece(raw[j][1], v + V, (const T*)nullptr);
-      if (norm) {
-        float ss = 0.0f;
+      for (int j = 0; j < HB; ++j) {
+        const int hh = h4 + j;
+        if (hh >= g.hpu) break;
+        const int h = h0 + hh;
+        const bool on = live && h < heads;
+        f2 v[V];
+        unpack_piece(raw[j][0], v, (const T*)nullptr);
+        unpack_piece(raw[j][1], v + V / 2, (const T*)nullptr);
+        if (norm) {
+          f2 ss = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) ss += v[i] * v[i];
-        const float r = rsqrtf(head_sum<LPH>(ss) * (1.0f / DH) + a.eps);
+          for (int i = 0; i < V; ++i) ss = fma2(v[i], v[i], ss);
+          const float2 sh = halves(ss);
+          const float r = rsqrtf(head_sum<LPH>(sh.x + sh.y) * (1.0f / DH) + a.eps);
+          const f2 rr = pair(r, r);
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) v[i] *= r * w[i];
-      }
-      if (rot) rotate<V, kInter>(v, c, s, 1.0f);
-      if (!kServe || part == PART_Q) {
-        if (on) {
-          T* out = (T*)(part == PART_Q ? a.q_out : a.k_out) + ((int64_t)row * heads + h) * DH;
-          store_piece(out + sub * V, v);
-          store_piece(out + DH / 2 + sub * V, v + V);
+          for (int i = 0; i < V; ++i) v[i] = mul2(v[i], mul2(rr, w[i]));
         }
-      } else {
-        const bool is_k = part == PART_K;
-        const int64_t at = page * (is_k ? g.c.k_page_stride : g.c.v_page_stride) +
-                           off * (is_k ? g.c.k_token_stride : g.c.v_token_stride) +
-                           h * (is_k ? g.c.k_head_stride : g.c.v_head_stride);
-        if (g.c.k_scale == nullptr) {
+        if (rot) rotate<V, kInter>(v, cs);
+        if (!kServe || part == PART_Q) {
           if (on) {
-            T* out = (T*)(is_k ? g.c.k : g.c.v) + at;
+            T* out = (T*)(part == PART_Q ? a.q_out : a.k_out) + ((int64_t)row * heads + h) * DH;
             store_piece(out + sub * V, v);
-            store_piece(out + DH / 2 + sub * V, v + V);
+            store_piece(out + DH / 2 + sub * V, v + V / 2);
           }
-        } else {  // one scale per (token, head): its largest magnitude maps to 448
-          float m = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 2 * V; ++i) m = fmaxf(m, fabsf(v[i]));
-          m = head_max<LPH>(m);
-          // (at least the smallest normal number, whose reciprocal is finite)
-          const float sc = m > 0.0f ? fmaxf(m / 448.0f, 1.17549435e-38f) : 1.0f, inv = 1.0f / sc;
-          if (on) {
-            uint8_t* out = (uint8_t*)(is_k ? g.c.k : g.c.v) + at;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint16_t q[V / 2];
-#pragma unroll
-              for (int i = 0; i < V / 2; ++i)
-                q[i] = e4m3_pair(v[half * V + 2 * i] * inv, v[half * V + 2 * i + 1] * inv);
-              uint2 u8;
-              u8.x = q[0] | ((uint32_t)q[1] << 16);
-              u8.y = q[V / 2 - 2] | ((uint32_t)q[V / 2 - 1] << 16);
-              *reinterpret_cast<uint2*>(out + half * (DH / 2) + sub * V) = u8;
+        } else {
+          const bool is_k = part == PART_K;
+          const int64_t at = page * (is_k ? g.c.k_page_stride : g.c.v_page_stride) +
+                             off * (is_k ? g.c.k_token_stride : g.c.v_token_stride) +
+                             h * (is_k ? g.c.k_head_stride : g.c.v_head_stride);
+          if (g.c.k_scale == nullptr) {
+            if (on) {
+              T* out = (T*)(is_k ? g.c.k : g.c.v) + at;
+              store_piece(out + sub * V, v);
+              store_piece(out + DH / 2 + sub * V, v + V / 2);
             }
-            if (sub == 0)
-              (is_k ? g.c.k_scale : g.c.v_scale)[(page * g.c.page_size + off) * heads + h] = sc;
+          } else {  // one scale per (token, head): its largest magnitude maps to 448
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float2 f = halves(v[i]);
+              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            m = head_max<LPH>(m);
+            // (at least the smallest normal number, whose reciprocal is finite)
+            const float sc = m > 0.0f ? fmaxf(m / 448.0f, 1.17549435e-38f) : 1.0f, inv = 1.0f / sc;
+            if (on) {
+              uint8_t* out = (uint8_t*)(is_k ? g.c.k : g.c.v) + at;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint16_t q[V / 2];
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                  const float2 f = halves(mul2(v[half * (V / 2) + i], pair(inv, inv)));
+                  q[i] = e4m3_pair(f.x, f.y);
+                }
+                uint2 u8;
+                u8.x = q[0] | ((uint32_t)q[1] << 16);
+                u8.y = q[V / 2 - 2] | ((uint32_t)q[V / 2 - 1] << 16);
+                *reinterpret_cast<uint2*>(out + half * (DH / 2) + sub * V) = u8;
+              }
+              if (sub == 0)
+                (is_k ? g.c.k_scale : g.c.v_scale)[(page * g.c.page_size + off) * heads + h] = sc;
+            }
           }
         }
       }
-     }
     }
   }
 }
@@ -307,7 +386,7 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
 template <typename T, int DH, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2)
 qk_bwd_kernel(const __grid_constant__ KArgs g) {
-  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH, HB = Geo<T>::kBatch / 2;
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH;
   __shared__ float red[kThreads / 32][DH];
   const QkArgs& a = g.a;
   const int part = (int)blockIdx.x < g.nb[0] ? PART_Q : PART_K;
@@ -324,22 +403,35 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
   const int sub = threadIdx.x % LPH, chunks = cdiv(heads, g.hpu);
   const int units = rows * chunks;  // at most the rows' heads: below 2^31 / head_dim
 
-  float w[2 * V], dw[2 * V];
+  f2 w[V], dw[V];
+  load_weights<V>(wp, sub * V, DH / 2 + sub * V, w);
   unsigned long long fr[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    w[i] = w[V + i] = 1.0f;
-    dw[i] = dw[V + i] = 0.0f;
-    if (wp) {
-      w[i] = wp[sub * V + i];
-      w[V + i] = wp[DH / 2 + sub * V + i];
-    }
+    dw[i] = 0;
     fr[i] = rot ? turn_fraction(a.inv_freq[pair_freq<T, DH, kInter>(sub, i)]) : 0ull;
   }
   const int first = blk * UPB, step = g.nb[part] * UPB;
   const bool slots = part == PART_Q && a.sorted_slot;
   int next = first + threadIdx.x / LPH;  // the next unit, and its row's slot
   int next_slot = slots && next < units ? a.sorted_slot[unit_row(next, chunks)] : 0;
+  uint4 ahead[4];
+  auto fetch = [&](int u, int hh) {  // head hh of unit u
+    const int row = u < units ? unit_row(u, chunks) : 0, h = (u - row * chunks) * g.hpu + hh;
+    const T* yp = dy + row * ldy + h * DH + sub * V;
+    const T* xp = x + row * ldx + h * DH + sub * V;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ahead[i] = make_uint4(0, 0, 0, 0);
+    if (u < units && h < heads) {
+      ahead[0] = *reinterpret_cast<const uint4*>(yp);
+      ahead[1] = *reinterpret_cast<const uint4*>(yp + DH / 2);
+      if (a.norm) {
+        ahead[2] = *reinterpret_cast<const uint4*>(xp);
+        ahead[3] = *reinterpret_cast<const uint4*>(xp + DH / 2);
+      }
+    }
+  };
+  fetch(next, 0);
   for (int u0 = first; u0 < units; u0 += step) {
     const int u = next;
     bool live = u < units;
@@ -348,26 +440,6 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
     const int slot = slots ? next_slot : row;
     next = u <= units - step ? u + step : units;
     if (slots && next < units) next_slot = a.sorted_slot[unit_row(next, chunks)];
-    const T* xr = x + row * ldx;
-    const T* yr = dy + row * ldy;
-    uint4 raw[HB][4];
-    auto fetch = [&](int hh) {
-#pragma unroll
-      for (int j = 0; j < HB; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[j][i] = make_uint4(0, 0, 0, 0);
-        if (live && hh + j < g.hpu && h0 + hh + j < heads) {
-          const int at = (h0 + hh + j) * DH + sub * V;
-          raw[j][0] = *reinterpret_cast<const uint4*>(yr + at);
-          raw[j][1] = *reinterpret_cast<const uint4*>(yr + at + DH / 2);
-          if (a.norm) {
-            raw[j][2] = *reinterpret_cast<const uint4*>(xr + at);
-            raw[j][3] = *reinterpret_cast<const uint4*>(xr + at + DH / 2);
-          }
-        }
-      }
-    };
-    fetch(0);
     int t = row;
     if (live && part == PART_Q) {
       if (slot < 0 || slot >= rows) {
@@ -377,51 +449,43 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
       t = slot / a.kslots;
     }
     const int pos = live && rot ? a.positions[t] : 0;
-    float c[V], s[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      c[i] = 1.0f; s[i] = 0.0f;
-      if (rot) turn<T>(fr[i], pos, &c[i], &s[i]);
-    }
-    for (int h2 = 0; h2 < g.hpu; h2 += HB) {
-     if (h2 > 0) fetch(h2);
-#pragma unroll
-     for (int j = 0; j < HB; ++j) {
-      const int hh = h2 + j;
-      if (hh >= g.hpu) break;
+    Turn<V> cs;
+    turns<T, V>(fr, rot, pos, -1.0f, cs);
+    for (int hh = 0; hh < g.hpu; ++hh) {
       const int h = h0 + hh;
       const bool on = live && h < heads;
-      float v[2 * V], d[2 * V];
-      unpack_piece(raw[j][0], d, (const T*)nullptr);
-      unpack_piece(raw[j][1], d + V, (const T*)nullptr);
-      unpack_piece(raw[j][2], v, (const T*)nullptr);
-      unpack_piece(raw[j][3], v + V, (const T*)nullptr);
-      if (rot) rotate<V, kInter>(d, c, s, -1.0f);
+      f2 v[V], d[V];
+      unpack_piece(ahead[0], d, (const T*)nullptr);
+      unpack_piece(ahead[1], d + V / 2, (const T*)nullptr);
+      unpack_piece(ahead[2], v, (const T*)nullptr);
+      unpack_piece(ahead[3], v + V / 2, (const T*)nullptr);
+      if (hh + 1 < g.hpu) fetch(u, hh + 1);
+      else fetch(next, 0);
+      if (rot) rotate<V, kInter>(d, cs);
       if (a.norm) {
         // with r = 1 / sqrt(...) and wd = w du: dx = r wd - x r^3 mean(wd x)
-        float ss = 0.0f, dot = 0.0f, wd[2 * V];
+        f2 ss = 0, dot = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          wd[i] = w[i] * d[i];
-          ss += v[i] * v[i];
-          dot += wd[i] * v[i];
+        for (int i = 0; i < V; ++i) {
+          ss = fma2(v[i], v[i], ss);
+          dot = fma2(mul2(w[i], d[i]), v[i], dot);
         }
-        ss = head_sum<LPH>(ss);
-        dot = head_sum<LPH>(dot);
-        const float r = rsqrtf(ss * (1.0f / DH) + a.eps);
-        const float m = r * r * r * dot * (1.0f / DH);
+        const float2 sh = halves(ss), dh = halves(dot);
+        const float r = rsqrtf(head_sum<LPH>(sh.x + sh.y) * (1.0f / DH) + a.eps);
+        const float m = -(r * head_sum<LPH>(dh.x + dh.y)) * (1.0f / DH) * r * r;
+        const f2 rr = pair(r, r), mm = pair(m, m);
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          dw[i] += d[i] * r * v[i];
-          d[i] = r * wd[i] - v[i] * m;
+        for (int i = 0; i < V; ++i) {
+          const f2 rd = mul2(rr, d[i]);
+          dw[i] = fma2(rd, v[i], dw[i]);
+          d[i] = fma2(v[i], mm, mul2(rd, w[i]));
         }
       }
       if (on && dx) {
         T* out = dx + ((int64_t)row * heads + h) * DH;
         store_piece(out + sub * V, d);
-        store_piece(out + DH / 2 + sub * V, d + V);
+        store_piece(out + DH / 2 + sub * V, d + V / 2);
       }
-     }
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -430,7 +494,8 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < 2 * V; ++i) {
-    float v = dw[i];
+    const float2 f = halves(dw[i / 2]);
+    float v = i % 2 ? f.y : f.x;
 #pragma unroll
     for (int off = LPH; off < 32; off <<= 1) v += __shfl_xor_sync(kFull, v, off);
     if (lane < LPH) red[warp][(i < V ? 0 : DH / 2 - V) + sub * V + i] = v;
