@@ -1050,7 +1050,7 @@ int smoe_moa_decode(const void* q, int64_t ldq, const int32_t* sorted_slot, int 
   unsigned* err = error_word(&st);
   if (!err) return cuda_fail(st, "smoe_moa_decode");
   cudaStream_t s = (cudaStream_t)stream;
-  PROF("moa.decode", 3);
+  PROF("moa.decode", decode_kernels(c, kslots, q_heads, sorted_slot != nullptr));
   SMOE_TRY(launch_decode(q, ldq, c, sorted_slot, kslots, q_heads, o, lse, workspace, err, s), "smoe_moa_decode");
   return SMOE_OK;
 }

@@ -431,8 +431,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
   for (;;) {
     while (inflight < STAGES) {
       if (ld.left <= 0) {
-        if (!more || opened - closed == kFifo) break;
-        if (!waited) break;
+        if (!more || !waited || opened - closed == kFifo) break;
         unsigned r = 0;
         if (lane == 0) r = atomicAdd(a.fetched, 1u);
         r = __shfl_sync(kFull, r, 0) + W;
@@ -507,7 +506,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
           amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
           int ex = (int)((__float_as_uint(amax) >> 23) & 0xff) - 127;
-          ex = max(-100, min(100, ex));
+          ex = max(-100, min(126, ex));
           const float down = __uint_as_float((unsigned)(127 - ex) << 23);
           const float up = __uint_as_float((unsigned)(127 + ex) << 23);
 #pragma unroll
@@ -1010,7 +1009,22 @@ struct DecWorkspace {
   }
 };
 
+// Without a kernel before it where no batch that the tables can hold has work to fetch, and
+// its rows are few enough to be looked for (one sequence of 2048 tokens: 8.7 us of the host's
+// time, with that kernel 11.8; on the device the same, where it runs beside the next one).
+bool direct(const smoe_kv_cache& c, int workers, int items, int rows, bool slots) {
+  const int nr = workers / items;
+  const long long most = (long long)c.B * (cdiv(c.max_pages * c.page_size, kHalf) + kItemCost);
+  return nr >= 1 && most / nr < kFetch && (!slots || rows <= kDirectRows);
+}
+int items_of(const smoe_kv_cache& c, int G) { return c.kv_heads * cdiv(G, 8 * tiles_of(G)); }
+
 }  // namespace
+
+int decode_kernels(const smoe_kv_cache& c, int kslots, int q_heads, bool slots) {
+  const int G = kslots * (q_heads / c.kv_heads);
+  return direct(c, workers_of(tiles_of(G)), items_of(c, G), c.B * kslots, slots) ? 2 : 3;
+}
 
 size_t decode_workspace_bytes(int rows, int kv_heads, int G, int head_dim) {
   return DecWorkspace(rows, kv_heads, G, head_dim).bytes;
@@ -1055,13 +1069,9 @@ cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, co
   a.fetched = (unsigned*)(base + w.fetched);
   a.inv = (int32_t*)(base + w.inv);
   a.err = err;
-  // Without a kernel before it where no batch that the tables can hold has work to fetch, and
-  // its rows are few enough to be looked for (one sequence of 2048 tokens: 8.7 us of the host's
-  // time, with that kernel 11.8; on the device the same, where it runs beside the next one).
-  const int items = c.kv_heads * a.mts, nr = a.workers / items;
-  const long long most = (long long)c.B * (cdiv(c.max_pages * c.page_size, kHalf) + kItemCost);
-  a.direct = nr >= 1 && most / nr < kFetch && (!sorted_slot || rows <= kDirectRows);
-  a.jobs = a.direct ? nr * items : w.jobs;
+  const int items = items_of(c, a.G);
+  a.direct = direct(c, a.workers, items, rows, sorted_slot != nullptr);
+  a.jobs = a.direct ? a.workers / items * items : w.jobs;
   if (a.direct) {
     a.inv = nullptr;
   } else {

@@ -196,6 +196,7 @@ cudaError_t launch_cache_append(const QkArgs& a, cudaStream_t s);
 
 // Paged decode attention (decode.cu) of rows = B * kslots grouped rows (sorted_slot null:
 // row = slot), G = queries that share a key head.
+int decode_kernels(const smoe_kv_cache& c, int kslots, int q_heads, bool slots);  // launches of a call
 size_t decode_workspace_bytes(int rows, int kv_heads, int G, int head_dim);
 cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c,
                           const int32_t* sorted_slot, int kslots, int q_heads, void* o, float* lse,

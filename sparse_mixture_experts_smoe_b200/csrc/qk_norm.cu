@@ -14,9 +14,10 @@
 // and sines for all heads of the row.
 //
 // Forward, a lane asks for the pieces of kBatch heads before it uses the first, and for a
-// row's pieces before its position; backward, for the next head's (the next row's after a
-// row's last) before it uses those at hand.  Outputs may be the inputs, so the compiler
-// does not move loads across stores by itself.
+// row's pieces before its position: outputs may be the inputs, so the compiler does not move
+// loads across stores by itself.  Backward, whose sums and weights fill the registers, it
+// copies its pieces with cp.async into places of its own in shared memory, kSteps - 1 heads
+// ahead and across rows; no lane waits for another.
 //
 // Angles: far positions need more than fp32.  inv_freq / (2 pi) is held as a 64-bit
 // fixed-point fraction of a turn, so position * fraction modulo 2^64 is the angle with
@@ -25,9 +26,13 @@
 // Bound: the instructions of a pass over 84 MB (8192 tokens, 4 slots, 4 heads of 128 bf16;
 // 13 us at the copy rate): 14 us from L2, 20 from DRAM.  Two fp32 values to an instruction
 // took the forward from 15.1 to 14.0 us, one wave of 296 blocks instead of 1280 from 20.5
-// to 15.9, asking for four heads before the first is used from 28.6 to 20.5.  The backward
-// (126 MB, 19.5 us) takes 32 us: 128 registers a thread leave 16 warps on an SM, each with
-// one head ahead, which is about half of the reads in flight that the memory's rate needs.
+// to 15.9, asking for four heads before the first is used from 28.6 to 20.5 (rings as the
+// backward's: 15.8, and 24 us instead of 22 for prompts into an e4m3 cache).  The backward
+// (126 MB, 19.5 us) takes 27 us from L2, 30 from DRAM; with the next head in registers 31
+// and 35, because 16 warps on an SM then keep half of the reads in flight that the memory's
+// rate needs; with rings of six steps 29 and 31.
+#include <atomic>
+
 #include "tc_ptx.cuh"
 
 namespace smoe {
@@ -41,6 +46,7 @@ template <typename T>
 struct Geo {
   static constexpr int V = 16 / sizeof(T);  // values per 16-byte piece
   static constexpr int kBatch = 4;          // heads loaded ahead, forward
+  static constexpr int kSteps = 3;          // of the backward's rings, a head each
 };
 
 // Two neighbouring fp32 values in one register pair: products and sums of both in one
@@ -90,6 +96,10 @@ __device__ __forceinline__ void store_piece(bf16* p, const f2* v) {
   }
   *reinterpret_cast<uint4*>(p) = pack8(f);
 }
+
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int LPH>
 __device__ __forceinline__ float head_sum(float v) {
@@ -386,7 +396,8 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
 template <typename T, int DH, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2)
 qk_bwd_kernel(const __grid_constant__ KArgs g) {
-  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH;
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH, S = Geo<T>::kSteps;
+  extern __shared__ uint4 places[];  // [S][4][kThreads]
   __shared__ float red[kThreads / 32][DH];
   const QkArgs& a = g.a;
   const int part = (int)blockIdx.x < g.nb[0] ? PART_Q : PART_K;
@@ -415,23 +426,27 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
   const bool slots = part == PART_Q && a.sorted_slot;
   int next = first + threadIdx.x / LPH;  // the next unit, and its row's slot
   int next_slot = slots && next < units ? a.sorted_slot[unit_row(next, chunks)] : 0;
-  uint4 ahead[4];
-  auto fetch = [&](int u, int hh) {  // head hh of unit u
-    const int row = u < units ? unit_row(u, chunks) : 0, h = (u - row * chunks) * g.hpu + hh;
-    const T* yp = dy + row * ldy + h * DH + sub * V;
-    const T* xp = x + row * ldx + h * DH + sub * V;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ahead[i] = make_uint4(0, 0, 0, 0);
-    if (u < units && h < heads) {
-      ahead[0] = *reinterpret_cast<const uint4*>(yp);
-      ahead[1] = *reinterpret_cast<const uint4*>(yp + DH / 2);
-      if (a.norm) {
-        ahead[2] = *reinterpret_cast<const uint4*>(xp);
-        ahead[3] = *reinterpret_cast<const uint4*>(xp + DH / 2);
-      }
+  int put_unit = next, put_head = 0, put = 0, get = 0;  // the step that is asked for next; stages
+  auto ask = [&]() {
+    const bool there = put_unit < units;
+    const int row = there ? unit_row(put_unit, chunks) : 0, h = (put_unit - row * chunks) * g.hpu + put_head;
+    const bool on = there && h < heads;
+    const T* yp = on ? dy + row * ldy + h * DH + sub * V : dy;
+    const T* xp = on && a.norm ? x + row * ldx + h * DH + sub * V : dy;
+    const uint32_t at = smem_u32(&places[(4 * put) * kThreads + threadIdx.x]);
+    cp_async16(at, yp, on ? 16u : 0u);
+    cp_async16(at + 16 * kThreads, on ? yp + DH / 2 : yp, on ? 16u : 0u);
+    cp_async16(at + 32 * kThreads, xp, on && a.norm ? 16u : 0u);
+    cp_async16(at + 48 * kThreads, on && a.norm ? xp + DH / 2 : xp, on && a.norm ? 16u : 0u);
+    cp_commit();
+    put = put + 1 == S ? 0 : put + 1;
+    if (++put_head == g.hpu) {
+      put_head = 0;
+      put_unit = put_unit <= units - step ? put_unit + step : units;
     }
   };
-  fetch(next, 0);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) ask();
   for (int u0 = first; u0 < units; u0 += step) {
     const int u = next;
     bool live = u < units;
@@ -455,12 +470,14 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
       const int h = h0 + hh;
       const bool on = live && h < heads;
       f2 v[V], d[V];
-      unpack_piece(ahead[0], d, (const T*)nullptr);
-      unpack_piece(ahead[1], d + V / 2, (const T*)nullptr);
-      unpack_piece(ahead[2], v, (const T*)nullptr);
-      unpack_piece(ahead[3], v + V / 2, (const T*)nullptr);
-      if (hh + 1 < g.hpu) fetch(u, hh + 1);
-      else fetch(next, 0);
+      cp_wait<S - 2>();
+      const uint4* mine = places + (4 * get) * kThreads + threadIdx.x;
+      unpack_piece(mine[0], d, (const T*)nullptr);
+      unpack_piece(mine[kThreads], d + V / 2, (const T*)nullptr);
+      unpack_piece(mine[2 * kThreads], v, (const T*)nullptr);
+      unpack_piece(mine[3 * kThreads], v + V / 2, (const T*)nullptr);
+      get = get + 1 == S ? 0 : get + 1;
+      ask();  // into the stage of the step before this one
       if (rot) rotate<V, kInter>(d, cs);
       if (a.norm) {
         // with r = 1 / sqrt(...) and wd = w du: dx = r wd - x r^3 mean(wd x)
@@ -488,6 +505,7 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
       }
     }
   }
+  cp_wait<0>();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!want_dw) return;
   // this block's share of dw: lanes of equal `sub`, then the warps in order
@@ -569,12 +587,28 @@ cudaError_t append(const KArgs& g, cudaStream_t s) {
   else qk_fwd_kernel<bf16, DH, false, true><<<grid, kThreads, 0, s>>>(g);
   return cudaGetLastError();
 }
+// The attribute that allows the rings belongs to the kernel on a device and stays: set once
+// for each.
+template <void (*Kern)(KArgs)>
+cudaError_t launch_rings(const KArgs& g, int grid, cudaStream_t s) {
+  constexpr size_t smem = (size_t)Geo<bf16>::kSteps * 4 * kThreads * sizeof(uint4);
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (e == cudaSuccess && !(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  }
+  if (e != cudaSuccess) return e;
+  Kern<<<grid, kThreads, smem, s>>>(g);
+  return cudaGetLastError();
+}
 template <typename T, int DH>
 cudaError_t bwd(const KArgs& g, cudaStream_t s) {
   const int grid = g.nb[0] + g.nb[1];
-  if (g.a.interleaved) qk_bwd_kernel<T, DH, true><<<grid, kThreads, 0, s>>>(g);
-  else qk_bwd_kernel<T, DH, false><<<grid, kThreads, 0, s>>>(g);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = g.a.interleaved ? launch_rings<qk_bwd_kernel<T, DH, true>>(g, grid, s)
+                                        : launch_rings<qk_bwd_kernel<T, DH, false>>(g, grid, s);
   if (e != cudaSuccess || (!g.a.dwq && !g.a.dwk)) return e;
   // starts early and waits for the shares on the device
   cudaLaunchAttribute at{};

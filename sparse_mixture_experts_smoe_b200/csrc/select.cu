@@ -185,9 +185,7 @@ __device__ __forceinline__ float gate_of(const SelectArgs& a, float lf, float b,
     return a.scale * w;
   }
   const float top = a.score == SMOE_SCORE_SOFTMAX ? l : fminf(l, 0.0f);
-  float m = ok ? top : -INFINITY;
-#pragma unroll
-  for (int off = W / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+  const float m = warp_max(ok ? top : -INFINITY);
   w = ok ? expf(top - m) : 0.0f;
   if (a.score == SMOE_SCORE_SIGMOID && ok) w /= 1.0f + expf(-fabsf(l));
   float sum = w;
@@ -459,24 +457,26 @@ __device__ __forceinline__ int select_row32(const T* __restrict__ row, const Sel
 constexpr int per_sm(int nv) { return nv <= 8 ? 9 : 4; }
 template <typename T, int NV, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32, per_sm(NV))
-select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int C, int32_t* __restrict__ idx,
-              float* __restrict__ gates) {
+select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int lpg_log2, int n, int C,
+              int32_t* __restrict__ idx, float* __restrict__ gates) {
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = a.E / a.groups, in0 = lpg ? (lane & (lpg - 1)) * C : 0;
+  const int in0 = lpg ? (lane & (lpg - 1)) * C : 0;
   Lane p;
   p.lane = lane;
   p.lpg = lpg;
-  p.group = lpg ? lane / lpg : 0;
+  p.group = lane >> lpg_log2;
   p.e0 = p.group * n + in0;
   p.have = p.group < a.groups && lpg ? max(0, min(C, n - in0)) : 0;
   constexpr int VE = NV * sizeof(T) < 16 ? NV : 16 / sizeof(T);
   const bool wide = p.have == NV && ((a.ld | p.e0) & (VE - 1)) == 0;
   float b[NV], next[NV];
+  if (BIAS) {
+    constexpr int VB = NV < 4 ? NV : 4;
+    const bool wide_bias = p.have == NV && (p.e0 & (VB - 1)) == 0 && ((uintptr_t)a.bias & (4 * VB - 1)) == 0;
+    load_experts<float, NV>(a.bias + p.e0, p.have, wide_bias, b);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    b[i] = BIAS && i < p.have ? a.bias[p.e0 + i] : 0.0f;
-    if (!(b[i] > -INFINITY)) b[i] = -INFINITY;
+    for (int i = 0; i < NV; ++i) b[i] = usable(b[i]) ? b[i] : -INFINITY;
   }
   const int step = gridDim.x * kWarps;
   int t = blockIdx.x * kWarps + warp;
@@ -699,7 +699,9 @@ cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* ga
   const size_t smem = (size_t)kWarps * (a.E + a.groups) * sizeof(double);
   int lpg = a.groups <= 32 ? 32 : 0;
   while (lpg * a.groups > 32) lpg >>= 1;
-  const int C = lpg ? cdiv(a.E / a.groups, lpg) : 0;
+  int lg = 0;
+  while ((1 << lg) < lpg) ++lg;
+  const int n = a.E / a.groups, C = lpg ? cdiv(n, lpg) : 0;
   // 32 values are what fits a lane's registers beside their scores
   // One row for each warp, so that CTAs come and go while a row is ranked in 64 bits (16384
   // rows of 256 experts in groups: 27 us, with several rows a warp 31); with many experts
@@ -707,8 +709,8 @@ cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* ga
 #define SELECT(NV, L)                                                                             \
   const int rows = NV <= 8 ? 1 : cdiv(a.T, 148 * per_sm(NV) * kWarps);                            \
   const int grid = cdiv(a.T, kWarps * rows);                                                      \
-  a.bias ? select_kernel<T, NV, true><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates) \
-         : select_kernel<T, NV, false><<<grid, kWarps * 32, smem, s>>>(logits, a, L, C, idx, gates)
+  a.bias ? select_kernel<T, NV, true><<<grid, kWarps * 32, smem, s>>>(logits, a, L, lg, n, C, idx, gates) \
+         : select_kernel<T, NV, false><<<grid, kWarps * 32, smem, s>>>(logits, a, L, lg, n, C, idx, gates)
   if (lpg == 0 || C > 32) { SELECT(1, 0); }
   else if (C == 1) { SELECT(1, lpg); }
   else if (C == 2) { SELECT(2, lpg); }

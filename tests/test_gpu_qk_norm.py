@@ -212,6 +212,9 @@ APPEND = {
     "one_each_e4m3": ([5, 17, 0, 40], None, 7, 2, 2, 1, 64, True, True, "head"),
     "prompts": ([9, 30, 4], [9, 11, 0], 8, 3, 6, 2, 128, False, True, "both"),
     "prompts_e4m3": ([100, 3, 64], [70, 3, 1], 64, 1, 4, 4, 128, True, False, "token"),
+    # more sequences than a block lists; a few without new tokens
+    "many_prompts": ([3 + b % 7 for b in range(600)], [(b * 5) % 3 for b in range(600)], 4, 1, 1, 1, 64, False, False,
+                     "token"),
     "page_of_one": ([6, 2], [3, 2], 1, 2, 1, 1, 64, False, False, "head"),
 }
 
