@@ -960,6 +960,12 @@ cudaError_t launch(bool early, void (*kern)(P...), int grid, int threads, size_t
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Two on each of 148 SMs, or one row for each warp.
+int join_blocks(const DecArgs& a, int R) {
+  const long long rows = (long long)a.jobs * (a.G < R ? a.G : R), n = (rows + kJoinWarps - 1) / kJoinWarps;
+  return (int)(n < 296 ? n : 296);
+}
+
 template <int DH, int NT, bool F8>
 cudaError_t run(const DecArgs& a, cudaStream_t s) {
   using TL = Tile<DH, F8>;
@@ -978,8 +984,8 @@ cudaError_t run(const DecArgs& a, cudaStream_t s) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   }
-  if (e == cudaSuccess) e = launch(!a.direct, kern, 148 * PER_SM, kThreads, smem, s, a);
-  if (e == cudaSuccess) e = launch(true, decode_join_kernel<DH>, 296, 32 * kJoinWarps, 0, s, a, 8 * NT);
+  if (e == cudaSuccess) e = launch(!a.direct, kern, a.direct ? cdiv(a.jobs, kWarps) : 148 * PER_SM, kThreads, smem, s, a);
+  if (e == cudaSuccess) e = launch(true, decode_join_kernel<DH>, join_blocks(a, 8 * NT), 32 * kJoinWarps, 0, s, a, 8 * NT);
   return e;
 }
 template <int DH, bool F8>
@@ -1009,13 +1015,16 @@ struct DecWorkspace {
   }
 };
 
+// Units, with the items' costs, of one item of every sequence that the tables can hold.
+long long most_units(const smoe_kv_cache& c) {
+  return (long long)c.B * (cdiv(c.max_pages * c.page_size, kHalf) + kItemCost);
+}
 // Without a kernel before it where no batch that the tables can hold has work to fetch, and
 // its rows are few enough to be looked for (one sequence of 2048 tokens: 8.7 us of the host's
 // time, with that kernel 11.8; on the device the same, where it runs beside the next one).
 bool direct(const smoe_kv_cache& c, int workers, int items, int rows, bool slots) {
   const int nr = workers / items;
-  const long long most = (long long)c.B * (cdiv(c.max_pages * c.page_size, kHalf) + kItemCost);
-  return nr >= 1 && most / nr < kFetch && (!slots || rows <= kDirectRows);
+  return nr >= 1 && most_units(c) / nr < kFetch && (!slots || rows <= kDirectRows);
 }
 int items_of(const smoe_kv_cache& c, int G) { return c.kv_heads * cdiv(G, 8 * tiles_of(G)); }
 
@@ -1071,7 +1080,11 @@ cudaError_t launch_decode(const void* q, int64_t ldq, const smoe_kv_cache& c, co
   a.err = err;
   const int items = items_of(c, a.G);
   a.direct = direct(c, a.workers, items, rows, sorted_slot != nullptr);
-  a.jobs = a.direct ? a.workers / items * items : w.jobs;
+  a.jobs = w.jobs;
+  if (a.direct) {  // no more jobs, and blocks for them, than can have a unit
+    const long long ranges = most_units(c) / kLeast + 1, nr = a.workers / items;
+    a.jobs = (int)(ranges < nr ? ranges : nr) * items;
+  }
   if (a.direct) {
     a.inv = nullptr;
   } else {

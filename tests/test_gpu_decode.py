@@ -34,6 +34,8 @@ CASES = {
     # so much work for each warp that a part of it is fetched
     "fetched": ([12000, 9000, 11000, 10500, 10, 0], 16, 128, 4, 1, 64, False, "token"),
     "fetched_e4m3": ([12000, 9000, 11000, 10500, 10], 48, 128, 8, 2, 64, True, "head"),
+    # more key heads and query tiles than warps
+    "many_items": ([40], 16, 128, 320, 320, 64, False, "token"),
     "e4m3": ([300, 0, 64, 63], 48, 2, 8, 2, 128, True, "token"),
     "e4m3_one": ([1], 7, 1, 1, 1, 64, True, "head"),
     "e4m3_sixteen": ([400, 31], 16, 4, 4, 1, 64, True, "both"),
@@ -220,6 +222,27 @@ def test_decode_offsets_beyond_32_bits(f8):
     o2, lse2 = _run(p, k_cache=big[0], v_cache=big[1], block_table=table.cuda(), **kw)
     assert smoe.smoe_check() == 0
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_fetched_ranges_in_graphs_and_streams():
+    """The form with fetched ranges: captured once, replayed with lengths that need them and
+    lengths that do not, while another stream makes the same call."""
+    p = _problem(*CASES["fetched"])
+    a = _args(p)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = smoe.smoe_moa_decode(**a)
+    st = torch.cuda.Stream()
+    for lens in ([12000, 9000, 11000, 10500, 10, 0], [5, 0, 0, 1, 10, 0], [0] * 6, [11999, 8001, 1, 10500, 9, 0]):
+        a["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        st.wait_stream(torch.cuda.current_stream())
+        g.replay()
+        other = smoe.smoe_moa_decode(stream=st, **a)
+        now = smoe.smoe_moa_decode(**a)
+        st.synchronize()
+        for x in (other, now):
+            assert torch.equal(out[0], x[0]) and torch.equal(out[1], x[1])
+    assert smoe.smoe_check() == 0
 
 
 def test_decode_empty_batch():
