@@ -805,7 +805,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
 // tile): the share of the range that started the item, then those of the ranges after it.
 // A warp takes a row with up to kFew shares, else the CTA's warps take every kJoinWarps-th
 // share each and their sums are joined in order.
-constexpr int kJoinWarps = 8, kFew = 24;
+constexpr int kJoinWarps = 8, kFew = 48;
 
 template <int DH>
 struct Joined {
@@ -960,10 +960,10 @@ cudaError_t launch(bool early, void (*kern)(P...), int grid, int threads, size_t
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Two on each of 148 SMs, or one row for each warp.
+// Three on each of 148 SMs, or one row for each warp.
 int join_blocks(const DecArgs& a, int R) {
   const long long rows = (long long)a.jobs * (a.G < R ? a.G : R), n = (rows + kJoinWarps - 1) / kJoinWarps;
-  return (int)(n < 296 ? n : 296);
+  return (int)(n < 444 ? n : 444);
 }
 
 template <int DH, int NT, bool F8>
