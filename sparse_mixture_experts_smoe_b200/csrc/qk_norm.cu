@@ -25,8 +25,8 @@
 //
 // Bound: the instructions of a pass over 84 MB (8192 tokens, 4 slots, 4 heads of 128 bf16;
 // 13 us at the copy rate): 14 us from L2, 20 from DRAM.  Two fp32 values to an instruction
-// took the forward from 15.1 to 14.0 us, one wave of 296 blocks instead of 1280 from 20.5
-// to 15.9, asking for four heads before the first is used from 28.6 to 20.5 (rings as the
+// took the forward from 15.1 to 14.0 us, one wave of blocks instead of 1280 from 20.5 to
+// 15.9 (128 threads a block rather than 256: prompts 22 to 21 us), asking for four heads before the first is used from 28.6 to 20.5 (rings as the
 // backward's: 15.8, and 24 us instead of 22 for prompts into an e4m3 cache).  The backward
 // (126 MB, 19.5 us) takes 27 us from L2, 30 from DRAM; with the next head in registers 31
 // and 35, because 16 warps on an SM then keep half of the reads in flight that the memory's
@@ -39,8 +39,9 @@ namespace smoe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 256;
-constexpr int kBlocks = 2 * 148;  // two on each of 148 SMs; the backward's fixes the order of dw's sums
+// One wave of blocks on 148 SMs.  The backward's number fixes the order of dw's sums.
+constexpr int kFwdThreads = 128, kFwdBlocks = 4 * 148;
+constexpr int kThreads = 256, kBlocks = 2 * 148;
 
 template <typename T>
 struct Geo {
@@ -244,9 +245,9 @@ __device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
 }
 
 template <typename T, int DH, bool kInter, bool kServe>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, 4)
 qk_fwd_kernel(const __grid_constant__ KArgs g) {
-  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kThreads / LPH, HB = Geo<T>::kBatch;
+  constexpr int V = Geo<T>::V, LPH = DH / (2 * V), UPB = kFwdThreads / LPH, HB = Geo<T>::kBatch;
   const QkArgs& a = g.a;
   int part = PART_Q, blk = blockIdx.x;
   while (part < PART_V && blk >= g.nb[part]) blk -= g.nb[part++];
@@ -270,7 +271,7 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
   __shared__ int listed[kServe ? 2 * kListed + 1 : 1];
   const int *starts = a.starts, *lens = g.c.seq_lens;
   if (kServe && starts && g.c.B <= kListed) {  // the search for a row's sequence is a chain of reads
-    for (int i = threadIdx.x; i <= g.c.B; i += kThreads) {
+    for (int i = threadIdx.x; i <= g.c.B; i += kFwdThreads) {
       listed[i] = starts[i];
       if (i < g.c.B) listed[g.c.B + 1 + i] = lens[i];
     }
@@ -558,9 +559,9 @@ int heads_per_unit(long long rows, int heads, int lph) {
 int lanes_per_head(int head_dim, int es) { return head_dim * es / 32; }
 
 // All blocks are resident at once and share out the parts' units in proportion.
-void plan(KArgs& g, int head_dim, int es) {
+void plan(KArgs& g, int head_dim, int es, int threads, int most) {
   const QkArgs& a = g.a;
-  const int lph = lanes_per_head(head_dim, es), upb = kThreads / lph;
+  const int lph = lanes_per_head(head_dim, es), upb = threads / lph;
   const int heads = a.q_heads > a.kv_heads ? a.q_heads : a.kv_heads;
   g.hpu = heads_per_unit((long long)a.T * a.kslots, heads, lph);
   const long long rows[3] = {a.q ? (long long)a.T * a.kslots : 0, a.k ? a.T : 0, a.v ? a.T : 0};
@@ -570,21 +571,21 @@ void plan(KArgs& g, int head_dim, int es) {
     all += blocks[p];
   }
   for (int p = 0; p < 3; ++p)
-    g.nb[p] = (int)(all <= kBlocks || blocks[p] == 0 ? blocks[p] : 1 + blocks[p] * (kBlocks - 3) / all);
+    g.nb[p] = (int)(all <= most || blocks[p] == 0 ? blocks[p] : 1 + blocks[p] * (most - 3) / all);
 }
 
 template <typename T, int DH>
 cudaError_t fwd(const KArgs& g, cudaStream_t s) {
   const int grid = g.nb[0] + g.nb[1] + g.nb[2];
-  if (g.a.interleaved) qk_fwd_kernel<T, DH, true, false><<<grid, kThreads, 0, s>>>(g);
-  else qk_fwd_kernel<T, DH, false, false><<<grid, kThreads, 0, s>>>(g);
+  if (g.a.interleaved) qk_fwd_kernel<T, DH, true, false><<<grid, kFwdThreads, 0, s>>>(g);
+  else qk_fwd_kernel<T, DH, false, false><<<grid, kFwdThreads, 0, s>>>(g);
   return cudaGetLastError();
 }
 template <int DH>
 cudaError_t append(const KArgs& g, cudaStream_t s) {
   const int grid = g.nb[0] + g.nb[1] + g.nb[2];
-  if (g.a.interleaved) qk_fwd_kernel<bf16, DH, true, true><<<grid, kThreads, 0, s>>>(g);
-  else qk_fwd_kernel<bf16, DH, false, true><<<grid, kThreads, 0, s>>>(g);
+  if (g.a.interleaved) qk_fwd_kernel<bf16, DH, true, true><<<grid, kFwdThreads, 0, s>>>(g);
+  else qk_fwd_kernel<bf16, DH, false, true><<<grid, kFwdThreads, 0, s>>>(g);
   return cudaGetLastError();
 }
 // The attribute that allows the rings belongs to the kernel on a device and stays: set once
@@ -634,7 +635,7 @@ size_t qk_bwd_partial_floats(int T, int kslots, int q_heads, int kv_heads, int h
 cudaError_t launch_qk_fwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s) {
   KArgs g{};
   g.a = a;
-  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4);
+  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4, kFwdThreads, kFwdBlocks);
   if (dt == SMOE_BF16) return head_dim == 64 ? fwd<bf16, 64>(g, s) : fwd<bf16, 128>(g, s);
   return head_dim == 64 ? fwd<float, 64>(g, s) : fwd<float, 128>(g, s);
 }
@@ -643,14 +644,14 @@ cudaError_t launch_cache_append(const QkArgs& a, cudaStream_t s) {
   KArgs g{};
   g.a = a;
   g.c = *a.cache;
-  plan(g, g.c.head_dim, 2);
+  plan(g, g.c.head_dim, 2, kFwdThreads, kFwdBlocks);
   return g.c.head_dim == 64 ? append<64>(g, s) : append<128>(g, s);
 }
 
 cudaError_t launch_qk_bwd(const QkArgs& a, int head_dim, smoe_dtype dt, cudaStream_t s) {
   KArgs g{};
   g.a = a;
-  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4);
+  plan(g, head_dim, dt == SMOE_BF16 ? 2 : 4, kThreads, kBlocks);
   if (dt == SMOE_BF16) return head_dim == 64 ? bwd<bf16, 64>(g, s) : bwd<bf16, 128>(g, s);
   return head_dim == 64 ? bwd<float, 64>(g, s) : bwd<float, 128>(g, s);
 }
