@@ -937,10 +937,13 @@ decode_join_kernel(const __grid_constant__ DecArgs a, int R) {
   }
 }
 
-// Query tiles: 8 columns of the product for each 8 of the G rows, up to 32 in one pass
-// over the keys.
-int tiles_of(int G) { return G <= 8 ? 1 : G <= 16 ? 2 : G <= 24 ? 3 : 4; }
-
+// 8-column products of a query tile: the G rows of a key head in as few tiles as have up to
+// three each, of one size.  Four spill (32 queries: 69 us, as two tiles of two 63), fewer
+// read the keys more often (24 queries: one of three 51 us, two of two 61, three of one 66).
+int tiles_of(int G) {
+  const int columns = cdiv(G, 8);
+  return cdiv(columns, cdiv(columns, 3));
+}
 // CTAs on each of 148 SMs: three where the registers allow it (8 queries), else two.
 int workers_of(int nt) { return 148 * kWarps * (nt == 1 ? 3 : 2); }
 
@@ -993,8 +996,7 @@ cudaError_t run_nt(const DecArgs& a, cudaStream_t s) {
   switch (tiles_of(a.G)) {
     case 1: return run<DH, 1, F8>(a, s);
     case 2: return run<DH, 2, F8>(a, s);
-    case 3: return run<DH, 3, F8>(a, s);
-    default: return run<DH, 4, F8>(a, s);
+    default: return run<DH, 3, F8>(a, s);
   }
 }
 

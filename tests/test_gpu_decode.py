@@ -29,6 +29,7 @@ CASES = {
     "page_of_100": ([1000, 99, 100, 101], 100, 2, 6, 2, 128, False, "head"),
     "sixteen_queries": ([513, 40], 48, 8, 4, 2, 128, False, "both"),
     "thirty_two_queries": ([700, 129], 64, 8, 4, 1, 128, False, "token"),
+    "forty_one_queries": ([130, 17], 16, 41, 2, 2, 128, True, "token"),
     "ninety_queries": ([300, 64, 17], 32, 15, 12, 2, 128, False, "token"),
     "many_sequences": ([(37 * b) % 91 for b in range(300)], 16, 2, 1, 1, 64, False, "token"),
     # so much work for each warp that a part of it is fetched
