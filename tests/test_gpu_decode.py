@@ -35,6 +35,10 @@ CASES = {
     # so much work for each warp that a part of it is fetched
     "fetched": ([12000, 9000, 11000, 10500, 10, 0], 16, 128, 4, 1, 64, False, "token"),
     "fetched_e4m3": ([12000, 9000, 11000, 10500, 10], 48, 128, 8, 2, 64, True, "head"),
+    # sequences that are not split
+    "short_sequences": ([(7 * b) % 90 for b in range(100)], 16, 2, 2, 2, 128, False, "token"),
+    "short_e4m3": ([(11 * b) % 60 for b in range(250)], 7, 1, 2, 1, 64, True, "head"),
+    "short_empty": ([0] * 77 + [33, 1], 32, 1, 1, 1, 64, False, "token"),
     # more key heads and query tiles than warps
     "many_items": ([40], 16, 128, 320, 320, 64, False, "token"),
     "e4m3": ([300, 0, 64, 63], 48, 2, 8, 2, 128, True, "token"),
