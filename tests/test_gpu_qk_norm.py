@@ -364,3 +364,28 @@ def test_empty():
     _, _, dwq, dwk = smoe.smoe_moa_qk_norm_rope_bwd(e, e, e, e, None, 2, q_heads=1, kv_heads=1, wq=w,
                                                     wk=w)
     assert (dwq == 0).all() and (dwk == 0).all()
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+def test_append_e4m3_codes_are_the_quotients(dh):
+    """Scale amax / 448 and code e4m3(v / scale), each operation rounded in fp32 as
+    smoe_quantize_weights_fp8 does, to the bit: bf16 rows have many quotients half way
+    between two codes, which a product with the scale's reciprocal moves off the middle."""
+    B, kvh = 700, 3
+    g = torch.Generator().manual_seed(31)
+    size = torch.exp2(torch.randint(-110, 110, (B, 1), generator=g).float())
+    size[:B // 2] = 1.0
+    k, v = ((size * torch.randn(B, kvh * dh, generator=g)).to(BF) for _ in range(2))
+    kc, vc = _cache(B, 1, kvh, dh, True)
+    sc = [torch.zeros(B, 1, kvh, device="cuda") for _ in range(2)]
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    smoe.smoe_moa_cache_append(None, k.cuda(), v.cuda(), kc, vc, table, lens, None, 1, kvh, norm=False,
+                               k_scale=sc[0], v_scale=sc[1])
+    assert smoe.smoe_check() == 0
+    for x, codes, scale in ((k, kc, sc[0]), (v, vc, sc[1])):
+        x = x.float().view(B, kvh, dh)
+        s = x.abs().amax(-1) / 448.0
+        assert torch.equal(scale.cpu()[:, 0], s)
+        want = (x / s[..., None]).to(torch.float8_e4m3fn)
+        assert torch.equal(codes.cpu()[:, 0].view(torch.float8_e4m3fn).float(), want.float())
