@@ -42,8 +42,12 @@
 //
 // The second product takes P as two bf16 numbers, the rounded weight and what the rounding
 // left, so that a weight keeps 16 bits (one alone would cost the output as much again as
-// its own rounding; the second product's time is under 1%).  e4m3 values take P times
-// their scales in fp16, whose half step of 2^-11 is small beside the values' own 2^-4.
+// its own rounding; the second product's time is under 1%).  For an e4m3 cache P is the
+// weight times the value's scale and the codes are turned into bf16, exactly: a product with
+// fp16 would lose small weights beside the scale of another row, such as the 1 of a row of
+// zeros, below 2^-24 (4096 tokens under a zero row 12 above them: 15% of the output).  Keys
+// are multiplied in fp16, codes exact and queries scaled to [1, 2), where what falls below
+// 2^-24 of the largest is within the fp32 sum's own rounding.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -144,6 +148,12 @@ __device__ __forceinline__ uint32_t e4m3_to_half2(uint16_t v) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two e4m3 codes as bf16, which holds all of their values (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3_to_bf162(uint16_t v) {
+  const uint32_t h = e4m3_to_half2(v);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -596,9 +606,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
             if (F8 && !on) ks[h][e] = 1.0f;  // a scale that was not copied is 0
           }
       }
-      // The reference m of a query's weights: its largest score; with scaled values the
-      // largest score times the value's scale, so that the weights times the scales, which
-      // are rounded to fp16 for the second product, are at most 1.
+      // The reference m of a query's weights: its largest score.
       float top[NT][2];
       bool grows = false;
 #pragma unroll
@@ -608,17 +616,15 @@ decode_kernel(const __grid_constant__ DecArgs a) {
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ls = F8 ? fmaxf(__log2f(vs[h][e]), -100.0f) : 0.0f;
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               float& v = s[h][t][2 * e + j];
               if (F8) v *= qs[t][j] * ks[h][e];
-              top[t][j] = fmaxf(top[t][j], F8 ? v + ls : v);
+              top[t][j] = fmaxf(top[t][j], v);
             }
-        }
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
@@ -656,7 +662,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       const uint32_t vb = base + UNIT * TL::kPitch;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        uint32_t pf[NT][2], pr[NT][2];  // pr: what the rounding of pf left (bf16)
+        uint32_t pf[NT][2], pr[NT][2];  // pr: what the rounding of pf left
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float* w = s[h][t];
@@ -666,17 +672,12 @@ decode_kernel(const __grid_constant__ DecArgs a) {
             w[2 + j] = ex2(F8 ? w[2 + j] - ref[t][j] : fmaf(w[2 + j], qs[t][j], -ref[t][j]));
             l[t][j] += w[j] + w[2 + j];
           }
-          if (F8) {
-            pf[t][0] = transpose8(pack_f16(w[0] * vs[h][0], w[1] * vs[h][0]));
-            pf[t][1] = transpose8(pack_f16(w[2] * vs[h][1], w[3] * vs[h][1]));
-          } else {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t hi = pack_bf16(w[2 * e], w[2 * e + 1]);
-              pr[t][e] = transpose8(pack_bf16(w[2 * e] - __uint_as_float(hi << 16),
-                                              w[2 * e + 1] - __uint_as_float(hi & 0xffff0000u)));
-              pf[t][e] = transpose8(hi);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const float x = F8 ? w[2 * e] * vs[h][e] : w[2 * e], y = F8 ? w[2 * e + 1] * vs[h][e] : w[2 * e + 1];
+            const uint32_t hi = pack_bf16(x, y);
+            pr[t][e] = transpose8(pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+            pf[t][e] = transpose8(hi);
           }
         }
         const uint32_t vh = vb + h * kHalf * TL::kPitch;
@@ -704,12 +705,15 @@ decode_kernel(const __grid_constant__ DecArgs a) {
             for (int e = 0; e < 2; ++e) {
               uint32_t g[4];  // rows gr: even dims, rows gr + 8: odd dims
               const uint32_t e0 = __byte_perm(f[2 * e], 0, 0x3120), e1 = __byte_perm(f[2 * e + 1], 0, 0x3120);
-              g[0] = e4m3_to_half2((uint16_t)e0);
-              g[1] = e4m3_to_half2((uint16_t)(e0 >> 16));
-              g[2] = e4m3_to_half2((uint16_t)e1);
-              g[3] = e4m3_to_half2((uint16_t)(e1 >> 16));
+              g[0] = e4m3_to_bf162((uint16_t)e0);
+              g[1] = e4m3_to_bf162((uint16_t)(e0 >> 16));
+              g[2] = e4m3_to_bf162((uint16_t)e1);
+              g[3] = e4m3_to_bf162((uint16_t)(e1 >> 16));
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma16816<true>(oacc[t][k + e], g, pf[t][0], pf[t][1]);
+              for (int t = 0; t < NT; ++t) {
+                mma16816<false>(oacc[t][k + e], g, pf[t][0], pf[t][1]);
+                mma16816<false>(oacc[t][k + e], g, pr[t][0], pr[t][1]);
+              }
             }
           }
         }

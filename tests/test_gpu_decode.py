@@ -291,3 +291,69 @@ def test_decode_streams_and_graphs():
             now = smoe.smoe_moa_decode(**a)
             assert torch.equal(out[0], now[0]) and torch.equal(out[1], now[1])
     assert smoe.smoe_check() == 0
+
+
+# Relative error of an e4m3 cache's weight times its scale as two bf16 numbers: 2^-16, fp32
+# products 2^-24, and the score's.
+PAIR = 2.0 ** -16 + 2.0 ** -20 + SCORE
+
+
+def _with_scales(p, k_scale, v_scale, k_code, v_code):
+    """The problem with these scales and codes (all places hold numbers)."""
+    p["scales"] = k_scale.cuda(), v_scale.cuda()
+    p["kc"], p["vc"] = k_code.view(torch.uint8).cuda(), v_code.view(torch.uint8).cuda()
+    p["k"] = k_code.double() * k_scale.double()[..., None]
+    p["v"] = v_code.double() * v_scale.double()[..., None]
+
+
+def _close_pair(p, o, lse):
+    ref, rl, size = plain.decode(p["q"], p["k"], p["v"], p["table"], p["lens"], p["slots"], p["ks"], p["qh"])
+    assert ((o.cpu().double() - ref).abs() <= plain.HALF[BF] * ref.abs() + PAIR * size + 1e-37).all()
+    assert ((lse.cpu().double() - rl).abs() <= SCORE + plain.HALF[torch.float32] * rl.abs()).all()
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("above", [0, 6, 9, 12])
+@pytest.mark.parametrize("lens", [[30, 9, 32] * 20, [64, 40, 33] * 20, [2048, 700], [4096]],
+                         ids=["whole", "short", "split", "long"])
+@pytest.mark.parametrize("amax", [3.0, 1e-5])
+def test_decode_e4m3_zero_value_row_with_a_high_score(lens, above, dh, amax):
+    """A key that draws most of the weight and whose value row is 0, with the scale 1 that an
+    append gives such a row: the other tokens' small weights keep their bits."""
+    p = _problem(lens, 16, 2, 2, 1, dh, True, "token", seed=7)
+    g = torch.Generator().manual_seed(8)
+    shape = p["k"].shape
+    code = [(448.0 * (2 * torch.rand(shape, generator=g) - 1)).to(torch.float8_e4m3fn).float() for _ in range(2)]
+    scale = [(0.5 + torch.rand(shape[:3], generator=g)) * m / 448.0 for m in (1.7, amax)]
+    code[0][..., 0] = 0.0  # the first dimension is the sink's: queries hold 8 there
+    p["q"] = p["q"].float().view(-1, 2, dh).index_fill(2, torch.tensor([0]), 8.0).to(BF).view(p["q"].shape)
+    for b, n in enumerate(lens):
+        u = (5 * b + 3) % n
+        at = int(p["table"][b, u // 16]), u % 16
+        code[0][at] = 0.0
+        code[0][at][0, 0] = 448.0
+        scale[0][at] = above * math.sqrt(dh) / (8.0 * 448.0) if above else 1.0 / 448.0
+        code[1][at], scale[1][at] = 0.0, 1.0
+    _with_scales(p, *scale, *(c.to(torch.float8_e4m3fn) for c in code))
+    o, lse = _run(p)
+    assert smoe.smoe_check() == 0
+    _close_pair(p, o, lse)
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("lens", [[30, 9, 32] * 20, [64, 40, 33] * 20, [3000]], ids=["whole", "short", "split"])
+def test_decode_e4m3_scales_of_any_size(lens, dh):
+    """Value scales from 2^-60 to 2^20 side by side, all codes in use."""
+    p = _problem(lens, 7, 3, 2, 2, dh, True, "head", seed=9)
+    g = torch.Generator().manual_seed(10)
+    shape = p["k"].shape
+    k_code = (448.0 * (2 * torch.rand(shape, generator=g) - 1)).to(torch.float8_e4m3fn)
+    raw = torch.randint(0, 256, shape, generator=g).to(torch.uint8)
+    raw[(raw & 0x7f) == 0x7f] = 1  # no NaN; 1: the smallest
+    k_scale = (0.5 + torch.rand(shape[:3], generator=g)) * 1.7 / 448.0
+    v_scale = torch.exp2(80 * torch.rand(shape[:3], generator=g) - 60)
+    _with_scales(p, k_scale, v_scale, k_code, raw.view(torch.float8_e4m3fn))
+    p["kc"], p["vc"] = (_store(t.cpu(), "head") for t in (p["kc"], p["vc"]))
+    o, lse = _run(p)
+    assert smoe.smoe_check() == 0
+    _close_pair(p, o, lse)
