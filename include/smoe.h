@@ -403,6 +403,8 @@ int smoe_moa_qk_norm_rope_bwd(const smoe_qk_desc* desc, const void* dyq, int64_t
  * row gets o = 0 and lse = -inf.  A length outside [0, max_pages * page_size] is
  * clamped, a key on a page outside [0, num_pages) is left out, a slot that
  * sorted_slot does not name is not written; all three are reported.
+ *   A NaN in a query or in a key of its sequence gives NaN, output and lse; a NaN value gives
+ * NaN in its column, an infinite one infinity or NaN.  Places without a token are not used.
  *   q, o [B*kslots, q_heads*head_dim] bf16 (q's row stride ldq; o contiguous).
  * workspace: smoe_moa_decode_workspace_size(B, kslots, q_heads, kv_heads, head_dim)
  * bytes, 256-byte aligned; nothing in it is kept between calls.  The sums run in an

@@ -808,7 +808,9 @@ decode_kernel(const __grid_constant__ DecArgs a) {
 // Joins the shares of the items that several ranges hold, row by row (of 8 NT a query
 // tile): the share of the range that started the item, then those of the ranges after it.
 // A warp takes a row with up to kFew shares, else the CTA's warps take every kJoinWarps-th
-// share each and their sums are joined in order.
+// share each and their sums are joined in order.  A share without a score above -inf has the
+// sum 0 or, where a query or all of its keys are NaN, NaN: it is added like the others, with
+// the factor 0, so that NaN stays.
 constexpr int kJoinWarps = 8, kFew = 48;
 
 template <int DH>
@@ -841,18 +843,16 @@ __device__ __forceinline__ Joined<DH> join_shares(const DecArgs& a, int it, int 
         for (int k = 0; k < N; ++k) p[h][k] = a.part_o[at * DH + 32 * k + lane];
       }
     }
-    float up = r.top;
+    const float before = r.top;
 #pragma unroll
-    for (int h = 0; h < kAhead; ++h) up = fmaxf(up, s[h].x);
-    if (up == -INFINITY) continue;
-    const float al = r.top == -INFINITY ? 0.0f : ex2(r.top - up);
-    r.top = up;
+    for (int h = 0; h < kAhead; ++h) r.top = fmaxf(r.top, s[h].x);
+    const float up = r.top == -INFINITY ? 0.0f : r.top, al = ex2(before - up);
     r.sum *= al;
 #pragma unroll
     for (int k = 0; k < N; ++k) r.v[k] *= al;
 #pragma unroll
     for (int h = 0; h < kAhead; ++h) {
-      const float f = s[h].x == -INFINITY ? 0.0f : ex2(s[h].x - up);
+      const float f = ex2(s[h].x - up);
       r.sum += f * s[h].y;
 #pragma unroll
       for (int k = 0; k < N; ++k) r.v[k] += f * p[h][k];
@@ -924,9 +924,10 @@ decode_join_kernel(const __grid_constant__ DecArgs a, int R) {
       float top = -INFINITY, sum = 0.0f, v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, ml[w].x);
+      const float up = top == -INFINITY ? 0.0f : top;
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = ml[w].x == -INFINITY ? 0.0f : ex2(ml[w].x - top);
+        const float f = ex2(ml[w].x - up);
         sum += f * ml[w].y;
         v += f * sums[w][threadIdx.x];
       }

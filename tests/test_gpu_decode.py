@@ -357,3 +357,59 @@ def test_decode_e4m3_scales_of_any_size(lens, dh):
     o, lse = _run(p)
     assert smoe.smoe_check() == 0
     _close_pair(p, o, lse)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("lens", [[16, 9, 3] * 15, [40, 33, 16] * 15, [2048, 700], [20000]],
+                         ids=["whole", "short", "split", "long"])
+def test_decode_nan_queries_give_nan(lens, f8):
+    """A head whose query holds a NaN gives NaN, output and lse, whether its sequence lies in
+    one range or in several; the other heads keep their bits."""
+    p = _problem(lens, 16, 2, 4, 2, 64, f8, "token", seed=11)
+    want = _run(p)
+    rows = p["q"].shape[0]
+    p["q"] = p["q"].clone()
+    hit = torch.zeros(rows, 4, dtype=torch.bool)
+    for i in (0, rows // 2, rows - 1):
+        h = i % 4
+        p["q"][i, h * 64 + (7 * i) % 64] = math.nan
+        hit[i, h] = True
+    o, lse = (t.cpu() for t in _run(p))
+    assert smoe.smoe_check() == 0
+    o = o.view(rows, 4, 64)
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], want[0].cpu().view(rows, 4, 64)[~hit]) and torch.equal(lse[~hit], want[1].cpu()[~hit])
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("part", ["all", "middle", "one"])
+def test_decode_nan_keys_give_nan(f8, part):
+    """Keys of NaN: all of a sequence, all of several ranges, a single one."""
+    p = _problem([3000, 50, 64], 16, 2, 2, 1, 64, f8, "token", seed=12)
+    want = _run(p)
+    for b, n in ((0, 3000), (1, 50)):
+        for u in {"all": range(n), "middle": range(n // 3, n // 2), "one": [n // 2]}[part]:
+            at = int(p["table"][b, u // 16]), u % 16
+            p["kc"][at] = 0x7f if f8 else math.nan
+    o, lse = _run(p)
+    assert smoe.smoe_check() == 0
+    on = (p["slots"] // 2 < 2).cuda()
+    assert torch.isnan(o[on]).all() and torch.isnan(lse[on]).all()
+    assert torch.equal(o[~on], want[0][~on]) and torch.equal(lse[~on], want[1][~on])
+
+
+@pytest.mark.parametrize("lens", [[16, 9, 3] * 15, [2048, 700]], ids=["whole", "split"])
+def test_decode_nan_and_infinite_values_stay_in_their_column(lens):
+    p = _problem(lens, 16, 2, 2, 1, 64, False, "token", seed=14)
+    want = _run(p)[0].view(-1, 2, 64)
+    for b, value, at in ((0, math.nan, 5), (1, math.inf, 63)):
+        u = lens[b] // 2
+        p["vc"][int(p["table"][b, u // 16]), u % 16, 0, at] = value
+    o = _run(p)[0].view(-1, 2, 64)
+    assert smoe.smoe_check() == 0
+    of = p["slots"].cuda() // 2
+    assert torch.isnan(o[of == 0, :, 5]).all() and not torch.isfinite(o[of == 1, :, 63]).any()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[of == 0, :, 5] = True
+    hit[of == 1, :, 63] = True
+    assert torch.equal(o[~hit], want[~hit])
