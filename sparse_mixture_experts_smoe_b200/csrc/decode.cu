@@ -477,6 +477,7 @@ decode_kernel(const __grid_constant__ DecArgs a) {
       t0 = cp.tile;
       const int mt = cp.it % a.mts, kvh = cp.it / a.mts;
       if (a.slots && !a.inv) {
+        __syncwarp();  // every lane has written the item before: it read its rows here
         for (int i = lane; i < a.kslots; i += 32) sequence_rows[warp][i] = -1;
         __syncwarp();
         const int all = c.B * a.kslots;

@@ -413,3 +413,19 @@ def test_decode_nan_and_infinite_values_stay_in_their_column(lens):
     hit[of == 0, :, 5] = True
     hit[of == 1, :, 63] = True
     assert torch.equal(o[~hit], want[~hit])
+
+
+def test_decode_many_short_items_for_each_warp():
+    """Items that follow one another in a warp, each with the rows of its own sequence, where
+    nothing between two of them makes the lanes wait (whole pages, one unit of 16 keys a
+    product) and not all lanes have a row to write."""
+    for ks, heads, dh in ((3, 64, 128), (2, 48, 128), (5, 64, 64)):
+        p = _problem([1 + (5 * b) % 40 for b in range(90)], 16, ks, heads, heads, dh, False, "token", seed=15)
+        a = _args(p)
+        o, lse = smoe.smoe_moa_decode(**a)
+        assert smoe.smoe_check() == 0
+        _close(p, o, lse)
+        for _ in range(20):
+            again = smoe.smoe_moa_decode(**a)
+            assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+        assert smoe.smoe_check() == 0
