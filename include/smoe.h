@@ -347,6 +347,8 @@ int smoe_moa_attn_bwd(const void* q, const void* k, const void* v, const void* o
  * lddyk) and the forward's q, k: dq, dk (contiguous, overwritten), and dwq, dwk
  * [head_dim] fp32 (overwritten; NULL to skip), summed in an order fixed by the sizes.
  * A part (q with dyq, dq, dwq; k likewise) is left out when its dy is NULL.
+ * A row whose slot is out of range is skipped here too: its row of dq is left as it was,
+ * and it adds nothing to dwq.
  * workspace: smoe_moa_qk_norm_rope_bwd_workspace_size(desc) bytes.
  * ------------------------------------------------------------------------ */
 typedef struct {

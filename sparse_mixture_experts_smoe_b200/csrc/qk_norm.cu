@@ -487,7 +487,11 @@ qk_bwd_kernel(const __grid_constant__ KArgs g) {
       const bool on = live && h < heads;
       f2 v[V], d[V];
       cp_wait<S - 2>();
-      const uint4* mine = places + (4 * get) * kThreads + threadIdx.x;
+      uint4* mine = places + (4 * get) * kThreads + threadIdx.x;
+      if (!live) {  // a skipped row, whatever it holds, adds nothing to dw
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine[i * kThreads] = make_uint4(0, 0, 0, 0);
+      }
       unpack_piece(mine[0], d, (const T*)nullptr);
       unpack_piece(mine[kThreads], d + V / 2, (const T*)nullptr);
       unpack_piece(mine[2 * kThreads], v, (const T*)nullptr);

@@ -389,3 +389,23 @@ def test_append_e4m3_codes_are_the_quotients(dh):
         assert torch.equal(scale.cpu()[:, 0], s)
         want = (x / s[..., None]).to(torch.float8_e4m3fn)
         assert torch.equal(codes.cpu()[:, 0].view(torch.float8_e4m3fn).float(), want.float())
+
+
+def test_backward_leaves_skipped_rows_out_of_the_weights():
+    """A row whose slot is out of range adds nothing to dwq: the bits of a run in which the
+    row's upstream gradient is 0, whatever the row holds."""
+    for name in ("slots", "fp32", "many"):
+        p = _problem(name, 9)
+        q, k, slots, dq, dk = _gpu(p, "q", "k", "slots", "dq", "dk")
+        rows = [0, 5, q.shape[0] - 1]
+        none = dq.clone()
+        none[rows] = 0
+        want = smoe.smoe_moa_qk_norm_rope_bwd(none, dk, q, k, slots, p["ks"], **_kw(p))
+        bad, x, dy = slots.clone(), q.clone(), dq.clone()
+        bad[rows] = torch.tensor([-1, slots.numel(), 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+        x[rows[0]], dy[rows[1]] = math.nan, math.inf
+        got = smoe.smoe_moa_qk_norm_rope_bwd(dy, dk, x, k, bad, p["ks"], **_kw(p))
+        assert smoe.smoe_check() == -4 and smoe.smoe_check() == 0
+        assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+        keep = [i for i in range(q.shape[0]) if i not in rows]
+        assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1], want[1])
