@@ -434,10 +434,12 @@ __device__ __forceinline__ int select_row32(const T* __restrict__ row, const Sel
   }
   if (BIAS) {
     const int below = __shfl_down_sync(kFull, rank, 1);
-    const float hi = __int_as_float(rank ^ ((rank >> 31) & 0x7fffffff));
-    const float lo = __int_as_float(below ^ ((below >> 31) & 0x7fffffff));
+    auto value = [](int r) -> float { return __int_as_float(r ^ ((r >> 31) & 0x7fffffff)); };
     // (a rank of -inf loses its last bits to NaN, no rank is one too: neither is near)
-    const bool near_by = p.lane < a.k && lo > -INFINITY && !(hi - lo > near + kRound * fabsf(hi));
+    auto near_each = [&](float hi, float lo) -> bool {
+      return lo > -INFINITY && !(hi - lo > near + kRound * fabsf(hi));
+    };
+    const bool near_by = p.lane < a.k && near_each(value(rank), value(below));
     if (__any_sync(kFull, near_by)) {  // equal logits and biases are equal in 64 bits as well
       float lm = 0.0f, bm = 0.0f;
       if (mine >= 0) {
@@ -445,7 +447,20 @@ __device__ __forceinline__ int select_row32(const T* __restrict__ row, const Sel
         bm = a.bias[mine];
       }
       const float ln = __shfl_down_sync(kFull, lm, 1), bn = __shfl_down_sync(kFull, bm, 1);
-      close_by = close_by || (near_by && !(lm == ln && bm == bn));
+      const bool equal = lm == ln && bm == bn;
+      close_by = close_by || (near_by && !equal);
+      // the last selected rank and the next are equal: so must be all that are near them
+      if (__any_sync(kFull, near_by && equal && p.lane == a.k - 1)) {
+        const float last = value(__shfl_sync(kFull, rank, a.k - 1));
+        lm = __shfl_sync(kFull, lm, a.k - 1);
+        bm = __shfl_sync(kFull, bm, a.k - 1);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {  // what is left in this lane
+          if (key[i] == INT_MIN || !near_each(last, value(PACK ? key[i] & ~7 : key[i]))) continue;
+          const int e = p.e0 + (PACK ? 7 - (key[i] & 7) : place[i]);
+          close_by = close_by || finite_top(to_f(row[e])) != lm || a.bias[e] != bm;
+        }
+      }
     }
   }
   if (__any_sync(kFull, close_by)) return -2;

@@ -248,3 +248,37 @@ def test_select_in_a_graph_and_on_another_stream():
         gr.replay()
         want = smoe.smoe_route_select(buf, 6, score="sigmoid")
         assert torch.equal(idx, want[0]) and torch.equal(gates, want[1])
+
+
+def _few_ranks(T, E, high, seed):
+    """Rows of logits far out, where fp32 scores are all alike, in few values (many ties)."""
+    g = torch.Generator().manual_seed(seed)
+    return (high + torch.randint(0, 3, (T, E), generator=g)).float()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [8, 64, 200, 512, 1001])
+def test_select_ties_at_the_border_before_a_near_third(E, dtype):
+    """The last selected rank and the next one are equal, and one behind them is not, but
+    lies higher in 64 bits: scores that fp32 rounds to one number."""
+    k = min(E - 3, 8)
+    logits = torch.zeros(3, E)
+    logits[0, :3] = torch.tensor([20.0, 20.0, 21.0])
+    logits[1, -3:] = torch.tensor([20.0, 20.0, 21.0])
+    logits[2, [0, E // 2, E - 1]] = torch.tensor([20.0, 20.0, 21.0])
+    _check(logits.to(dtype), torch.zeros(E), 1, "sigmoid", True, 1.0, 1, 1, 2)
+    _check(logits.to(dtype), torch.zeros(E), 2, "sigmoid", False, 1.0, 1, 1, 2)
+    for kk in (1, k):
+        _check(_few_ranks(30, E, 18.0, 20).to(dtype), torch.zeros(E), kk, "sigmoid", True, 1.0, 1, 1, 2)
+        _check(_few_ranks(30, E, -20.0, 21).to(dtype), torch.full((E,), 0.5), kk, "sigmoid", True, 1.0, 1, 1, 2)
+        # softmax: one expert has all of the mass, and a bias that keeps it behind the others
+        logits, b = _few_ranks(30, E, -20.0, 22), torch.full((E,), 0.5)
+        logits[:, E // 3], b[E // 3] = 0.0, -5.0
+        _check(logits.to(dtype), b, kk, "softmax", False, 1.0, 1, 1, 2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E,groups", [(48, 4), (256, 8), (640, 4)])
+def test_select_ties_in_groups(E, groups, dtype):
+    for high, bias in ((18.0, 0.0), (-20.0, 0.5)):
+        _check(_few_ranks(20, E, high, 23).to(dtype), torch.full((E,), bias), 5, "sigmoid", True, 1.0, groups, 2, 2)
