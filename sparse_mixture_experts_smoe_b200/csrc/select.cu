@@ -363,6 +363,8 @@ __device__ __forceinline__ int select_row32(const T* __restrict__ row, const Sel
       const float size = fmaxf(fabsf(v1), v2 > -INFINITY ? fabsf(v2) : 0.0f);
       const float most = warp_max(there && v1 > -INFINITY ? size : 0.0f);
       close_by = out > -INFINITY && !(in - out > 2.0f * (near + kRound * most));
+      // a sum that leaves fp32's range still ranks before a group without experts
+      close_by = close_by || (v2 > -INFINITY && gs == -INFINITY);
     }
   }
   // INT_MIN: not to be chosen (an unavailable expert's -inf ranks above that)

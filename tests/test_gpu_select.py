@@ -282,3 +282,26 @@ def test_select_ties_at_the_border_before_a_near_third(E, dtype):
 def test_select_ties_in_groups(E, groups, dtype):
     for high, bias in ((18.0, 0.0), (-20.0, 0.5)):
         _check(_few_ranks(20, E, high, 23).to(dtype), torch.full((E,), bias), 5, "sigmoid", True, 1.0, groups, 2, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(16, 4), (96, 4), (512, 8), (96, 48)])
+def test_select_group_sums_beyond_fp32(score, E, groups):
+    """Biases of the type's lowest and largest value: the sum of two leaves fp32's range, and
+    a group that has experts still ranks before one that has none."""
+    low, high = torch.finfo(F32).min, torch.finfo(F32).max
+    n = E // groups
+    logits, _ = _inputs(6, E, F32, False, 24)
+    none = torch.full((E,), -math.inf)
+    for fill in (low, high):
+        for top_groups in (1, 2):
+            for where in ([groups - 1], [1, groups - 1], [0, 2], list(range(1, groups))):
+                b = none.clone()
+                for g in where:
+                    b[g * n:(g + 1) * n] = fill
+                _check(logits, b, 2, score, True, 1.0, groups, top_groups, 2)
+                b[where[-1] * n] = math.inf
+                _check(logits, b, 2, score, True, 1.0, groups, top_groups, 2)
+    b = torch.full((E,), low)
+    b[(groups - 1) * n:] = low * 0.75
+    _check(logits, b, 2, score, True, 1.0, groups, 1, 2)
