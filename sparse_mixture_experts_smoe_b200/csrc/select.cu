@@ -469,7 +469,8 @@ __device__ __forceinline__ int select_row32(const T* __restrict__ row, const Sel
   return p.lane < a.k ? mine : -1;
 }
 
-// One warp per row, its next row's logits on their way; lpg = 0: every row in 64 bits.
+// One warp per row, with many experts to a lane for several, whose logits are asked for a
+// row ahead; lpg = 0: every row in 64 bits.
 // The ranking in 64 bits is rare, so it may spill: nine CTAs of the common path fit an SM.
 constexpr int per_sm(int nv) { return nv <= 8 ? 9 : 4; }
 template <typename T, int NV, bool BIAS>
@@ -495,10 +496,11 @@ select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int lpg_log2,
 #pragma unroll
     for (int i = 0; i < NV; ++i) b[i] = usable(b[i]) ? b[i] : -INFINITY;
   }
-  const int step = gridDim.x * kWarps;
+  constexpr bool SEVERAL = NV > 8;  // rows to a warp: of over 100 experts, so t + step fits
+  const int step = SEVERAL ? gridDim.x * kWarps : 0;
   int t = blockIdx.x * kWarps + warp;
   if (t < a.T && lpg) load_experts<T, NV>(logits + (size_t)t * a.ld + p.e0, p.have, wide, next);
-  for (; t < a.T; t += step) {
+  for (; t < a.T; t = SEVERAL ? t + step : a.T) {
     const T* row = logits + (size_t)t * a.ld;
     float mx = -INFINITY, den = 0.0f;
     int e = -2;
@@ -506,7 +508,7 @@ select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int lpg_log2,
       float l[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) l[i] = usable(next[i]) ? finite_top(next[i]) : -INFINITY;
-      if (t + step < a.T) load_experts<T, NV>(row + (size_t)step * a.ld + p.e0, p.have, wide, next);
+      if (SEVERAL && t + step < a.T) load_experts<T, NV>(row + (size_t)step * a.ld + p.e0, p.have, wide, next);
       e = select_row32<T, NV, BIAS>(row, a, p, l, b, &mx, &den);
       if (NV <= 8 && e == -2) e = select_row64_wide<T, NV>(row, a, p);
     }
@@ -711,6 +713,9 @@ select_bwd_wide_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t
   }
 }
 
+// Blocks of n rows each for T rows, up to 2^31 - 1 of them.
+int blocks(int T, int n) { return (int)(((long long)T + n - 1) / n); }
+
 template <typename T>
 cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* gates, cudaStream_t s) {
   const size_t smem = (size_t)kWarps * (a.E + a.groups) * sizeof(double);
@@ -724,8 +729,8 @@ cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* ga
   // rows of 256 experts in groups: 27 us, with several rows a warp 31); with many experts
   // a lane several, whose logits are asked for a row ahead (1024 experts: 119 us against 135).
 #define SELECT(NV, L)                                                                             \
-  const int rows = NV <= 8 ? 1 : cdiv(a.T, 148 * per_sm(NV) * kWarps);                            \
-  const int grid = cdiv(a.T, kWarps * rows);                                                      \
+  const int rows = NV <= 8 ? 1 : blocks(a.T, 148 * per_sm(NV) * kWarps);                          \
+  const int grid = blocks(a.T, kWarps * rows);                                                    \
   a.bias ? select_kernel<T, NV, true><<<grid, kWarps * 32, smem, s>>>(logits, a, L, lg, n, C, idx, gates) \
          : select_kernel<T, NV, false><<<grid, kWarps * 32, smem, s>>>(logits, a, L, lg, n, C, idx, gates)
   if (lpg == 0 || C > 32) { SELECT(1, 0); }
@@ -745,11 +750,11 @@ cudaError_t select_bwd(const T* logits, const SelectArgs& a, const int32_t* idx,
   constexpr int V = 16 / sizeof(T);
   const int pieces = a.E / V;
   if (a.E % V || a.ld % V || pieces > 8 * 32) {  // rows that are not whole 16-byte pieces
-    select_bwd_kernel<T><<<cdiv(a.T, kWarps), kWarps * 32, 0, s>>>(logits, a, idx, gates, dgates, dl, err);
+    select_bwd_kernel<T><<<blocks(a.T, kWarps), kWarps * 32, 0, s>>>(logits, a, idx, gates, dgates, dl, err);
     return cudaGetLastError();
   }
 #define SELECT_BWD(LPR, NP)                                                                              \
-  select_bwd_wide_kernel<T, LPR, NP><<<cdiv(a.T, kWarps * 32 / LPR), kWarps * 32, 0, s>>>(logits, a, idx, \
+  select_bwd_wide_kernel<T, LPR, NP><<<blocks(a.T, kWarps * 32 / LPR), kWarps * 32, 0, s>>>(logits, a, idx, \
                                                                                           gates, dgates, dl, err)
   if (pieces <= 8) SELECT_BWD(8, 1);
   else if (pieces <= 16) SELECT_BWD(16, 1);

@@ -305,3 +305,17 @@ def test_select_group_sums_beyond_fp32(score, E, groups):
     b = torch.full((E,), low)
     b[(groups - 1) * n:] = low * 0.75
     _check(logits, b, 2, score, True, 1.0, groups, 1, 2)
+
+
+def test_select_most_rows():
+    """2^31 - 1 rows of one expert: the row count and its next multiple of a block's rows leave 32 bits."""
+    T = 2 ** 31 - 1
+    x = torch.zeros((T, 1), dtype=BF, device="cuda")
+    idx = torch.full((T, 1), 7, dtype=torch.int32, device="cuda")
+    gates = torch.full((T, 1), 7.0, device="cuda")
+    smoe.smoe_route_select(x, 1, score="sigmoid", topk_idx=idx, gates=gates)
+    assert smoe.smoe_check() == 0
+    assert not bool(idx.any()) and bool((gates == 1).all())
+    gates.fill_(0.5)
+    dl = smoe.smoe_route_select_bwd(x, idx, gates, gates, score="sigmoid", renorm=False)
+    assert smoe.smoe_check() == 0 and bool((dl == 0.125).all())
