@@ -257,7 +257,7 @@ smoe_kv_cache kv_cache(const Tensor& k, const Tensor& v, const Tensor& table, co
     expect(t, name, dt, shape, dev);
     if (shape[3] > 1 && t.stride(3) != 1) value_error(std::string(name) + " must have unit stride inside a head");
     for (int j = 0; j < 3; ++j) {
-      st[i][j] = t.stride(j);
+      st[i][j] = shape[j] > 1 ? t.stride(j) : 0;  // one place: its stride is of no account
       if (written && st[i][j] == 0 && shape[j] > 1)
         value_error(std::string(name) + " is written and must not be an expanded tensor");
     }

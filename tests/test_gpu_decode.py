@@ -429,3 +429,25 @@ def test_decode_many_short_items_for_each_warp():
             again = smoe.smoe_moa_decode(**a)
             assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
         assert smoe.smoe_check() == 0
+
+
+def test_decode_cache_with_one_key_head_of_any_stride():
+    """A dimension of one has no stride that counts."""
+    for f8 in (False, True):
+        p = _problem([70, 9], 16, 2, 2, 1, 64, f8, "token", seed=13)
+        want = _run(p)
+        pages = p["kc"].shape[0]
+        odd = [torch.empty(pages, 16, 64, 1, dtype=t.dtype, device="cuda").transpose(2, 3) for t in (p["kc"], p["vc"])]
+        for x, t in zip(odd, (p["kc"], p["vc"])):
+            x.copy_(t)
+            assert x.stride(2) == 1
+        o, lse = _run(p, k_cache=odd[0], v_cache=odd[1])
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        k = torch.ones(2, 64, dtype=BF, device="cuda")
+        kw = dict(k_scale=p["scales"][0], v_scale=p["scales"][1], norm=False)
+        a = _args(p)
+        smoe.smoe_moa_cache_append(None, k, k, odd[0], odd[1], a["block_table"], a["seq_lens"], None, 1, 1, **kw)
+        smoe.smoe_moa_cache_append(None, k, k, p["kc"], p["vc"], a["block_table"], a["seq_lens"], None, 1, 1, **kw)
+        assert smoe.smoe_check() == 0
+        assert all(torch.equal(x.view(torch.uint8), t.view(torch.uint8)) for x, t in
+                   zip((odd[0].contiguous(), odd[1].contiguous()), (p["kc"], p["vc"])))
