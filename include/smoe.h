@@ -43,6 +43,7 @@
  *     in a per-device error word that smoe_check reports.
  *   - Alignment: d, f, K and N must be multiples of 8 (16-byte rows for the
  *     tensor-memory-accelerator copies); every tensor start 16-byte aligned.
+ *   - Outputs must not overlap inputs, unless an entry point says that they may.
  *   - Several calls may run concurrently on different streams as long as they
  *     do not share workspaces or outputs.
  *   - Size limits (checked on the host, SMOE_ERR_INVALID_ARG beyond them):

@@ -94,6 +94,20 @@ void* out(OptTensor& t, const char* name, ScalarType dt, IntArrayRef shape, int 
   t = make(shape, dt, dev);
   return t->data_ptr();
 }
+// Refuses a given output (contiguous) that shares memory with the rows of an input: outputs
+// are written while inputs are still read.
+void apart(const OptTensor& out, const char* name, const Tensor& in, const char* input) {
+  if (!out || out->numel() == 0 || in.numel() == 0) return;
+  const bool rows = in.dim() == 2 && in.size(0) > 1;
+  const uintptr_t o = (uintptr_t)out->data_ptr(), i = (uintptr_t)in.data_ptr(), oe = o + out->nbytes();
+  const uintptr_t step = rows ? (uintptr_t)in.stride(0) * in.element_size() : 0;
+  const uintptr_t width = (rows ? in.size(1) : in.numel()) * in.element_size();
+  const uintptr_t last = rows ? in.size(0) - 1 : 0;
+  if (oe <= i || o >= i + last * step + width) return;
+  // the first row that ends behind the output's start
+  const uintptr_t r = o < i + width || step == 0 ? 0 : (o - i - width) / step + 1;
+  if (i + r * step < oe) value_error(std::string(name) + " must not overlap " + input);
+}
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((at::DeviceIndex)dev).stream(); }
 // The device that a call's tensors are on is current while it runs.
 struct On {
@@ -116,6 +130,8 @@ std::pair<Tensor, Tensor> route_select(const Tensor& logits, const OptTensor& bi
     check(smoe_route_select(x.p, as_int(x.ld, "the row stride of logits"), b, as_int(T, "T"), as_int(E, "E"), k, score,
                             renorm, scale, groups, top_groups, group_top, dt, nullptr, nullptr, nullptr));
   const int64_t shape[2] = {T, k};
+  apart(idx, "topk_idx", logits, "logits");
+  apart(gates, "gates", logits, "logits");
   void* i = out(idx, "topk_idx", I32, shape, on.dev);
   void* g = out(gates, "gates", F32, shape, on.dev);
   check(smoe_route_select(x.p, as_int(x.ld, "the row stride of logits"), b, as_int(T, "T"), as_int(E, "E"), k, score,
@@ -136,6 +152,10 @@ Tensor route_select_bwd(const Tensor& logits, const Tensor& idx, const Tensor& g
   void* i = at(idx, "topk_idx", I32, shape, on.dev);
   void* g = at(gates, "gates", F32, shape, on.dev);
   void* dg = at(dgates, "dgates", F32, shape, on.dev);
+  apart(dlogits, "dlogits", logits, "logits");
+  apart(dlogits, "dlogits", idx, "topk_idx");
+  apart(dlogits, "dlogits", gates, "gates");
+  apart(dlogits, "dlogits", dgates, "dgates");
   void* dl = out(dlogits, "dlogits", logits.scalar_type(), full, on.dev);
   check(smoe_route_select_bwd(x.p, as_int(x.ld, "the row stride of logits"), (int32_t*)i, (float*)g, (float*)dg,
                               as_int(T, "T"), as_int(E, "E"), as_int(k, "k"), score, renorm, scale, dt, dl,
@@ -172,6 +192,12 @@ QkCall qk_call(const OptTensor& q, const OptTensor& k, int kslots, int q_heads, 
   return c;
 }
 
+// The same, but for an output that is its input.
+void apart_or_same(const OptTensor& out, const char* name, const Tensor& in, const char* input) {
+  if (out && out->data_ptr() == in.data_ptr() && in.is_contiguous() && out->nbytes() == in.nbytes()) return;
+  apart(out, name, in, input);
+}
+
 std::pair<OptTensor, OptTensor> qk_norm_rope_fwd(const OptTensor& q, const OptTensor& k, const OptTensor& slots,
                                                  const OptTensor& positions, const OptTensor& inv_freq,
                                                  const OptTensor& wq, const OptTensor& wk, OptTensor q_out,
@@ -180,6 +206,12 @@ std::pair<OptTensor, OptTensor> qk_norm_rope_fwd(const OptTensor& q, const OptTe
   const QkCall c = qk_call(q, k, kslots, q_heads, kv_heads, norm, interleaved, eps);
   const On on(k ? *k : *q);
   if ((!q && q_out) || (!k && k_out)) value_error("an output without its input");
+  if (q) apart_or_same(q_out, "q_out", *q, "q");
+  if (k) apart_or_same(k_out, "k_out", *k, "k");
+  if (q && k) {
+    apart(q_out, "q_out", *k, "k");
+    apart(k_out, "k_out", *q, "q");
+  }
   Rows x, y;
   void *xo = nullptr, *yo = nullptr;
   if (q) {
@@ -297,6 +329,7 @@ OptTensor cache_append(const OptTensor& q, const Tensor& k, const Tensor& v, con
   cache_tensor(k_cache);
   const On on(k_cache);
   const smoe_kv_cache c = kv_cache(k_cache, v_cache, table, lens, k_scale, v_scale, true, on.dev);
+  if (c.k == c.v && k_cache.numel() > 0) value_error("k_cache and v_cache must not overlap");
   matrix(k, "k");
   const int64_t T = k.size(0), dh = c.head_dim;
   const Rows y = rows_of(k, "k", BF16, T, c.kv_heads * dh, on.dev);
@@ -306,6 +339,9 @@ OptTensor cache_append(const OptTensor& q, const Tensor& k, const Tensor& v, con
   if (q) {
     const int64_t shape[2] = {T * kslots, q_heads * dh};
     x = rows_of(*q, "q", BF16, shape[0], shape[1], on.dev);
+    apart_or_same(q_out, "q_out", *q, "q");
+    apart(q_out, "q_out", k, "k");
+    apart(q_out, "q_out", v, "v");
     xo = out(q_out, "q_out", BF16, shape, on.dev);
   } else if (q_out) {
     value_error("q_out without q");
@@ -329,6 +365,8 @@ std::pair<Tensor, Tensor> decode(const Tensor& q, const Tensor& k_cache, const T
   const int64_t shape[2] = {(int64_t)c.B * kslots, (int64_t)q_heads * c.head_dim}, heads[2] = {shape[0], q_heads};
   const Rows x = rows_of(q, "q", BF16, shape[0], shape[1], on.dev);
   const int32_t* s = opt<int32_t>(slots, "sorted_slot", I32, {shape[0]}, on.dev);
+  apart(o, "o", q, "q");
+  apart(lse, "lse", q, "q");
   void* op = out(o, "o", BF16, shape, on.dev);
   void* lp = out(lse, "lse", F32, heads, on.dev);
   const int64_t bytes[1] = {

@@ -110,3 +110,45 @@ def test_append_and_decode():
             with pytest.raises((ValueError, TypeError, smoe.SmoeError)):
                 smoe.smoe_moa_cache_append(**{**good, **bad}, **a)
         assert (a["k_cache"].float() == 0).all() and smoe.smoe_check() == 0
+
+
+def test_outputs_over_inputs():
+    """A given output that shares memory with an input is refused, but for the calls that
+    work in place."""
+    x = _z(8, 16)
+    with pytest.raises(ValueError, match="overlap"):
+        smoe.smoe_route_select(x, 16, gates=x)
+    with pytest.raises(ValueError, match="overlap"):
+        smoe.smoe_route_select(x, 16, topk_idx=x.view(torch.int32))
+    idx, gates = smoe.smoe_route_select(x, 2)
+    with pytest.raises(ValueError, match="overlap"):
+        smoe.smoe_route_select_bwd(x, idx, gates, gates, dlogits=x)
+    with pytest.raises(ValueError, match="overlap"):  # the rows of a wider tensor
+        smoe.smoe_route_select_bwd(_z(8, 32)[:, :16], idx, x[0].view(8, 2), gates, dlogits=x)
+    buf = _z(3, 8, 128, dtype=BF).flatten()
+    q, k = buf[:1024].view(8, 128), buf[1024:1536].view(4, 128)
+    kw = dict(q_heads=2, kv_heads=2)
+    smoe.smoe_moa_qk_norm_rope_fwd(q, k, None, 2, q_out=q, k_out=k, **kw)
+    smoe.smoe_moa_qk_norm_rope_fwd(q, k, None, 2, q_out=buf[1536:2560].view(8, 128), **kw)
+    for o in (dict(q_out=buf[64:1088].view(8, 128)), dict(k_out=buf[1152:1664].view(4, 128)),
+              dict(q_out=buf[512:1536].view(8, 128)), dict(k_out=buf[:512].view(4, 128))):
+        with pytest.raises(ValueError, match="overlap"):
+            smoe.smoe_moa_qk_norm_rope_fwd(q, k, None, 2, **o, **kw)
+    a = _cache_args()
+    rows = _z(9, 128, dtype=BF)
+    a["block_table"] += 1
+    good = dict(sorted_slot=None, kslots=1, q_heads=2)
+    smoe.smoe_moa_cache_append(rows[:3], rows[3:6], rows[6:], q_out=rows[:3], norm=False, **good, **a)
+    for at in (1, 3, 5, 6):
+        with pytest.raises(ValueError, match="overlap"):
+            smoe.smoe_moa_cache_append(rows[:3], rows[3:6], rows[6:], q_out=rows[at:at + 3], norm=False, **good, **a)
+    smoe.smoe_moa_decode(rows[:3], o=rows[3:6], **good, **a)
+    with pytest.raises(ValueError, match="overlap"):
+        smoe.smoe_moa_decode(rows[:3], o=rows[:3], **good, **a)
+    with pytest.raises(ValueError, match="overlap"):
+        smoe.smoe_moa_decode(rows[:3], lse=rows.view(torch.float32)[0, :6].view(3, 2), **good, **a)
+    # a cache whose keys and values are one tensor cannot be written
+    a["v_cache"] = a["k_cache"]
+    with pytest.raises(ValueError, match="overlap"):
+        smoe.smoe_moa_cache_append(None, rows[:3], rows[:3], norm=False, **good, **a)
+    assert smoe.smoe_check() == 0
