@@ -362,12 +362,13 @@ _native = None
 
 
 def _calls():
-    """The compiled checks (built in-tree like the library if missing); raises without them."""
+    """The compiled checks (built in-tree like the library if missing, or if built for another
+    torch); raises without them."""
     global _native
     if _native is None:
         lib()
-        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
-            from . import build as _build
+        from . import build as _build
+        if _build.binding_stale():
             _build.build()
         _native = importlib.import_module("._binding", __name__)
     return _native

@@ -23,6 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsmoe.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(BUILD, "binding.txt")  # what _binding.so was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -54,9 +55,25 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _binding_for() -> str:
+    """What the built module depends on beside its sources: torch and the interpreter."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def binding_stale() -> bool:
+    """No module, or one built for another torch or Python (it would fail to load)."""
+    if not os.path.exists(BINDING):
+        return True
+    if not os.path.exists(BINDING_STAMP):  # a package without its build folder: taken as it is
+        return False
+    with open(BINDING_STAMP) as f:
+        return f.read() != _binding_for()
+
+
 def _build_binding(force: bool) -> None:
     inputs = (BINDING_SRC, os.path.join(INCLUDE, "smoe.h"))
-    if not force and os.path.exists(BINDING) and \
+    if not force and not binding_stale() and os.path.exists(BINDING_STAMP) and \
             os.path.getmtime(BINDING) >= max(os.path.getmtime(p) for p in inputs):
         return
     import sysconfig
@@ -74,6 +91,8 @@ def _build_binding(force: bool) -> None:
                                        "-ltorch_python"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
