@@ -9,28 +9,28 @@
 // 4 head_dim bytes (bf16) per key and head leave the tensor pipe far from busy.
 //
 // Split: a sequence is cut into units of 16 H keys (H = 2 where a row is 128 bytes or
-// less, which spreads a unit's own instructions over more keys: e4m3, 128 sequences of
-// 8000 tokens 160 -> 123 us).  The sequences' units in a row, with kItemCost units' worth
-// of time for a sequence's own start and end, are cut into ranges; a job is a range and an
-// item (a key head and a tile of queries), and a warp's.  Neighbouring warps have the items
-// of one range, because the key heads' rows of a token lie next to one another in a page
-// (64 sequences of up to 16384 bf16 tokens, 4 heads: 184 us, with ranges of single heads
-// 188; 128 of 8000 in e4m3: 106 and 112).  No warp waits for another.
+// less, which spreads a unit's own instructions over more keys; when chosen, e4m3, 128
+// sequences of 8000 tokens: 123 us, with H = 1 160).  The sequences' units in a row, with
+// kItemCost units' worth of time for a sequence's own start and end, are cut into ranges;
+// a job is a range and an item (a key head and a tile of queries), and a warp's.
+// Neighbouring warps have the items of one range, because the key heads' rows of a token
+// lie next to one another in a page. No warp waits for another.
 //
 // Where a warp has 32 units and more, an eighth of the work goes in smaller ranges that a
 // warp fetches from a counter when it has finished, because SMs do not get equal shares of
-// the memory's rate (equal runs alone ended up to 20% apart; those 64 sequences: 184 us,
-// without fetched ranges 193, with a quarter 191).  So a ragged batch and a single long
-// sequence load the GPU alike.  A sequence that lies in one range is finished there; the
-// shares of the others go to the workspace and a second kernel joins them in the order of
-// the ranges.  Ranges and the order of all sums follow from sizes and lengths alone: a
-// batch gives the same bits every time.
+// the memory's rate: equal runs alone end up to 20% apart (when chosen, 64 sequences of up
+// to 16384 tokens: 184 us, without fetched ranges 193, with a quarter 191).  So a ragged
+// batch and a single long sequence load the GPU alike.  A sequence that lies in one range
+// is finished there; the shares of the others go to the workspace and a second kernel
+// joins them in the order of the ranges.  Ranges and the order of all sums follow from
+// sizes and lengths alone: a batch gives the same bits every time.
 //
-// Time: 128 sequences of up to 4096 tokens, 537 MB, 83 us at the copy rate: 99 us, of which
-// the units take 85 at 6.4 TB/s, the start up to the first keys 5 and the join 5 (reads
-// that wait for one another).  48 sequences of up to 8190 in e4m3, 105 MB, 16 us: 35 us;
-// seven units a warp do not hide its start and end.  One sequence of 2048 tokens: 11 us,
-// latency throughout.
+// Time: 128 sequences of up to 4096 tokens, 537 MB, 83 us at the copy rate: 99 to 105 us, of
+// which the units take 85 at 6.4 TB/s, the start up to the first keys 5 and the join 5
+// (reads that wait for one another).  64 of up to 16384, 1107 MB, 171 us: 187 to 194.  48 of up
+// to 8190 in e4m3, 105 MB, 16 us: 39.5; seven units a warp do not hide its start and end, and
+// 32 keys take 1100 instructions, for half of the bytes that a bf16 cache loads beside 950.
+// One sequence of 2048 tokens: 12 us, latency throughout.
 //
 // A warp copies its keys' rows with cp.async into its own ring in shared memory, units
 // ahead and across items, and keeps a running maximum m, sum l and accumulator O (one
@@ -99,8 +99,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 // A whole piece of a row that is read once and should leave L2 first: what the warps hand
-// to the joining kernel stays there (128 sequences of up to 4096 tokens: 99 us, without
-// 103; 24 queries to a key head: 48 and 54).
+// to the joining kernel stays there.
 __device__ __forceinline__ unsigned long long read_once() {
   unsigned long long policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));

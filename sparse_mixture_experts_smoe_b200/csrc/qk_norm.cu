@@ -23,14 +23,11 @@
 // fixed-point fraction of a turn, so position * fraction modulo 2^64 is the angle with
 // whole turns dropped exactly; its upper 32 bits go to sincospif (bf16: to sin.approx).
 //
-// Bound: the instructions of a pass over 84 MB (8192 tokens, 4 slots, 4 heads of 128 bf16;
-// 13 us at the copy rate): 14 us from L2, 20 from DRAM.  Two fp32 values to an instruction
-// took the forward from 15.1 to 14.0 us, one wave of blocks instead of 1280 from 20.5 to
-// 15.9 (128 threads a block rather than 256: prompts 22 to 21 us), asking for four heads before the first is used from 28.6 to 20.5 (rings as the
-// backward's: 15.8, and 24 us instead of 22 for prompts into an e4m3 cache).  The backward
-// (126 MB, 19.5 us) takes 27 us from L2, 30 from DRAM; with the next head in registers 31
-// and 35, because 16 warps on an SM then keep half of the reads in flight that the memory's
-// rate needs; with rings of six steps 29 and 31.
+// Bound: latency, then instructions.  A pass over 84 MB (8192 tokens, 4 slots, 4 heads of 128
+// bf16; 13 us at the copy rate) takes 20.5 us, 14 with the input in L2: SMs are active for
+// 74% of the launch and issue in 53% of those cycles; warps wait for loads and for fixed
+// latencies.  The backward (126 MB, 19.5 us) takes 30 us, 27 with the input in L2, at 83%
+// and 63%.  Two fp32 values go to an instruction, blocks are one wave.
 #include <atomic>
 
 #include "tc_ptx.cuh"

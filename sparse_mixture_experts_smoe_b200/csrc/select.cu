@@ -10,12 +10,14 @@
 // the lower id.  One warp has a row.  It ranks in 32 bits with scores whose error is
 // bounded, and where two ranks that decide the outcome lie closer together than that
 // bound (and are not equal because logit and bias are), it ranks the row again in 64 bits.
-// Logits of a normal distribution bring that about in one row of a thousand.
+// Logits of a normal distribution bring that about in one row of 1300.
 //
-// Bound: instructions.  16384 rows of 256 fp32 logits are 18 MB, 2.8 us at the copy rate;
-// they take 27 us, about 1000 instructions a row: 490 to load, score, order and write, 36
-// for each of the nine rounds, 208 for the groups (16384 x 256 without bias and groups,
-// k = 1: 13 us), and what the few rows in 64 bits add at the end, about 6 us.
+// Bound: instructions, and the rows in 64 bits at the end.  16384 rows of 256 fp32 logits in
+// 8 groups are 18 MB, 2.8 us at the copy rate; they take 25 us, 23 with the logits in L2,
+// and 970 instructions a row, issued in 73% of the cycles that SMs are active.  Without
+// groups 18 us, without bias too 14, and then with k = 1 11.  Rows without a near tie (one
+// row repeated) take 19: a row in 64 bits waits for its own exponentials and rounds while
+// the rest of the GPU has finished.
 #include <cfloat>
 #include <climits>
 
@@ -225,8 +227,7 @@ struct Lane {
   int lane, lpg, group, e0, have;
 };
 
-// select_row64 with the row's scores in registers, so that a lane's exponentials overlap (as
-// loops 32 us instead of 27 where one row of a thousand takes this path).
+// select_row64 with the row's scores in registers, so that a lane's exponentials overlap.
 template <typename T, int NV>
 __device__ __noinline__ int select_row64_wide(const T* __restrict__ row, const SelectArgs& a, const Lane p) {
   float lf[NV], b[NV];
@@ -725,9 +726,12 @@ cudaError_t select(const T* logits, const SelectArgs& a, int32_t* idx, float* ga
   while ((1 << lg) < lpg) ++lg;
   const int n = a.E / a.groups, C = lpg ? cdiv(n, lpg) : 0;
   // 32 values are what fits a lane's registers beside their scores
-  // One row for each warp, so that CTAs come and go while a row is ranked in 64 bits (16384
-  // rows of 256 experts in groups: 27 us, with several rows a warp 31); with many experts
-  // a lane several, whose logits are asked for a row ahead (1024 experts: 119 us against 135).
+  // One row for each warp, so that CTAs come and go while a row is ranked in 64 bits; with
+  // many experts a lane several, whose logits are asked for a row ahead (when this rule was
+  // made: 16384 rows of 256 experts in groups 27 us, with several rows a warp 31; of 1024
+  // experts 135 and 119).
+  // More than 32 groups, or 32 experts to a lane, rank every row in 64 bits from loops (256
+  // experts in 64 groups: 336 us).
 #define SELECT(NV, L)                                                                             \
   const int rows = NV <= 8 ? 1 : blocks(a.T, 148 * per_sm(NV) * kWarps);                          \
   const int grid = blocks(a.T, kWarps * rows);                                                    \
