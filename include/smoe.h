@@ -183,7 +183,8 @@ int smoe_route_bwd(const void* x, const void* w_r, const int32_t* topk_idx, cons
  *   softmax renorm: dl_e = g_e dg_e - g_e A / scale               (selected, else 0)
  *   sigmoid:        dl_e = g_e dg_e (1 - s_e)                     (selected, else 0)
  *   sigmoid renorm: dl_e = (g_e dg_e - g_e A / scale) (1 - s_e)   (selected, else 0)
- *   dlogits [T, E] dtype (contiguous, overwritten).  A gate of 0 passes nothing on.
+ *   dlogits [T, E] dtype (contiguous, overwritten).  A gate of 0 passes nothing on, and an
+ *   expert whose score is 0 (as an unavailable one's) gets 0 whatever A is.
  *   An id outside [0, E) is skipped and reported (SMOE_ERR_DATA); the ids of a row
  *   must be distinct, as the forward's are.
  * ------------------------------------------------------------------------ */

@@ -542,7 +542,7 @@ select_kernel(const T* __restrict__ logits, SelectArgs a, int lpg, int lpg_log2,
 //   sigmoid:       dl_j = g_j dg_j (1 - s_j)
 //   softmax:       dl_e = [e selected] g_e dg_e - p_e A      (every expert)
 // 1 - s = 1 / (1 + exp(l)).  A gate of 0 (an expert that was not available) passes
-// nothing on.
+// nothing on, and an expert whose p is 0 gets 0 even where A is NaN or infinite.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
 select_bwd_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t* __restrict__ idx,
@@ -583,8 +583,8 @@ select_bwd_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t* __r
   for (int i = lane; i < a.E; i += 32) {
     float d = 0.0f;
     if (dense) {
-      const float l = to_f(row[i]);
-      if (usable(l)) d = -(expf(finite_top(l) - mx) / den) * A;
+      const float l = to_f(row[i]), p = usable(l) ? expf(finite_top(l) - mx) / den : 0.0f;
+      if (p > 0.0f) d = -p * A;
     }
     out[i] = from_f<T>(d);
   }
@@ -593,7 +593,8 @@ select_bwd_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t* __r
     float d = 0.0f;
     const float l = to_f(row[e]);
     if (dense) {
-      d = gd - (usable(l) ? (expf(finite_top(l) - mx) / den) * A : 0.0f);
+      const float p = usable(l) ? expf(finite_top(l) - mx) / den : 0.0f;
+      d = gd - (p > 0.0f ? p * A : 0.0f);
     } else if (g != 0.0f) {
       d = a.renorm ? gd - g * (A / a.scale) : gd;
       if (a.score == SMOE_SCORE_SIGMOID) d *= 1.0f / (1.0f + expf(l));
@@ -675,7 +676,7 @@ select_bwd_wide_kernel(const T* __restrict__ logits, SelectArgs a, const int32_t
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[p][i] *= f;
+      for (int i = 0; i < V; ++i) x[p][i] = x[p][i] > 0.0f ? x[p][i] * f : 0.0f;
   } else {
 #pragma unroll
     for (int p = 0; p < NP; ++p)

@@ -319,3 +319,25 @@ def test_select_most_rows():
     gates.fill_(0.5)
     dl = smoe.smoe_route_select_bwd(x, idx, gates, gates, score="sigmoid", renorm=False)
     assert smoe.smoe_check() == 0 and bool((dl == 0.125).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [61, 64, 256])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_select_gradient_of_unavailable_experts_under_a_broken_upstream(E, dtype, bad):
+    """Masked experts get 0 from a NaN or infinite upstream gradient too, whether or not a
+    row is made of whole pieces; every available expert shows it."""
+    T, k = 9, 4
+    logits, _ = _inputs(T, E, dtype, False, 25)
+    mask = torch.rand(T, E, generator=torch.Generator().manual_seed(26)) < 0.4
+    logits[mask] = -math.inf
+    x = logits.cuda()
+    idx, gates = smoe.smoe_route_select(x, k, score="softmax", renorm=False)
+    dg = torch.ones(T, k, device="cuda")
+    want = smoe.smoe_route_select_bwd(x, idx, gates, dg, score="softmax", renorm=False).cpu()
+    dg[2, 1] = bad
+    dl = smoe.smoe_route_select_bwd(x, idx, gates, dg, score="softmax", renorm=False).cpu()
+    assert smoe.smoe_check() == 0
+    assert (dl[mask] == 0).all() and not torch.isfinite(dl[2][~mask[2]]).any()
+    keep = [t for t in range(T) if t != 2]
+    assert torch.equal(dl[keep], want[keep])
